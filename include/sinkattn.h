@@ -416,6 +416,114 @@ int sinkattn_decode_noalloc(sinkattn_dtype dt, int B, int Hq, int Hkv, int D, fl
                             const float *learnable_sink, void *out, float *lse_new,
                             float *sink_s, int num_splits, sinkattn_stream_t stream);
 
+/* ---- paged cache -------------------------------------------------------------
+ * A pool of pages shared by all sequences, in place of one ring a sequence: a
+ * page holds page_size consecutive positions of one sequence for every KV head,
+ * each head's rows in one contiguous block.  Position p of sequence b is row
+ * p % page_size of page block_table[b, p / page_size].
+ *   k_pages, v_pages  [n_pages, Hkv, page_size, D]: of the calls' type dt, or
+ *                  uint8 E4M3 codes (the 8-bit cache).  16-byte aligned.
+ *   k_scale, v_scale  float32 [n_pages, Hkv], finite and >= 0: value = code
+ *                  value x scale of the row's page and KV head.  NULL with the
+ *                  16-bit cache.
+ *   block_table    device int32 [B, max_pages].  Entries past a sequence's last
+ *                  page are not read.
+ *   cache_seqlens  device int32 [B]: tokens of sequence b, those of the call
+ *                  included (<= max_pages page_size).
+ *   page_size      16, 32, 64 or 128 (else SINKATTN_ERR_UNSUPPORTED).
+ *   D              64 or 128.  B, Hkv <= 65535; n_pages page_size Hkv and
+ *                  max_pages page_size < 2^31 (element offsets may pass 2^31).
+ * The struct is read on the host during the call.  An entry of block_table
+ * outside [0, n_pages) that a call needs, or a position past the table, sets
+ * SINKATTN_ERR_BOUNDS in the status word; its rows are neither read nor written. */
+typedef struct {
+    void *k_pages;
+    void *v_pages;
+    float *k_scale;
+    float *v_scale;
+    const int32_t *block_table;
+    const int32_t *cache_seqlens;
+    int32_t B;
+    int32_t n_pages;
+    int32_t page_size;
+    int32_t max_pages;
+    int32_t Hkv;
+    int32_t D;
+} sinkattn_paged_cache;
+
+/* sinkattn_paged_append -- new keys and values into a paged 16-bit cache, keys
+ * (and, if given, the tokens' queries) rotated to their positions on the way.
+ *   dt             SINKATTN_BF16 or SINKATTN_FP16 (FP32: UNSUPPORTED).
+ *   k, v           [T, Hkv, D], q [T, Hq, D] or NULL: packed new tokens; a
+ *                  token's heads are contiguous, tokens k_stride / v_stride /
+ *                  q_stride elements apart (multiples of 8; views of one fused
+ *                  projection are fine).
+ *   cu_new         device int32 [B + 1]: sequence b's new tokens are
+ *                  [cu_new[b], cu_new[b + 1]); rows past cu_new[B] are ignored
+ *                  and their outputs left as they are.  NULL: T = B, one token a
+ *                  sequence, and a sequence with cache_seqlens[b] <= 0 has none.
+ *                  The tokens are the sequence's last: the i-th of n has
+ *                  position cache_seqlens[b] - n + i.
+ *   rope           float32 [n_pos, rot_dim] or NULL (no rotation): cosines of
+ *                  the position's rot_dim / 2 angles, then their sines.  Pairs
+ *                  (a, b) -> (a cos - b sin, b cos + a sin) are elements
+ *                  (i, i + rot_dim / 2) of a head, or (2i, 2i + 1) with
+ *                  interleaved = 1; elements past rot_dim are copied.  rot_dim:
+ *                  a multiple of 16 in [16, D].  Computed in float32, rounded
+ *                  once.  A token whose position is >= n_pos or negative is not
+ *                  written (SINKATTN_ERR_BOUNDS).
+ *   q_out          [T, Hq, D] contiguous (may be q itself); with q.
+ *   k_out          [T, Hkv, D] contiguous or NULL: the rotated keys (for
+ *                  sinkattn_fwd over the new tokens of a prefill).
+ * A page that a call writes belongs to one sequence of the call (pages shared
+ * for reading only may repeat). */
+int sinkattn_paged_append(sinkattn_dtype dt, int T, int Hq, const sinkattn_paged_cache *cache,
+                          const void *k, long long k_stride, const void *v, long long v_stride,
+                          const void *q, long long q_stride, const int32_t *cu_new,
+                          const float *rope, int rot_dim, int n_pos, int interleaved, void *q_out,
+                          void *k_out, sinkattn_stream_t stream);
+
+/* sinkattn_paged_append_fp8 -- the same into the 8-bit cache.  A block (page, KV
+ * head) stores E4M3(value / s), round to nearest even, from the float32 rotated
+ * value; s is the block's scale, the smallest power of two 2^e (e >= -126) with
+ * amax <= 448 s over the finite magnitudes written to it (0 while they are all
+ * 0).  When a call adds rows to a block that holds earlier ones, s is the larger
+ * of the old scale and the new rows' own; if it grows, the earlier codes become
+ * E4M3(code old / s), exact but for codes that become subnormal.  Infinities
+ * saturate to +-448 s, NaN stays NaN.  A block's row 0 starts it afresh. */
+int sinkattn_paged_append_fp8(sinkattn_dtype dt, int T, int Hq, const sinkattn_paged_cache *cache,
+                              const void *k, long long k_stride, const void *v,
+                              long long v_stride, const void *q, long long q_stride,
+                              const int32_t *cu_new, const float *rope, int rot_dim, int n_pos,
+                              int interleaved, void *q_out, void *k_out, sinkattn_stream_t stream);
+
+/* sinkattn_paged_decode -- one query token per sequence over a paged 16-bit
+ * cache, sinkattn_decode's computation and results with position j of sequence b
+ * visible if j < cache_seqlens[b] and, with window > 0, j < n_sink or
+ * j >= cache_seqlens[b] - window (the StreamingLLM set; pages wholly outside it
+ * are not read).
+ *   q              [B, Hq, D] of type dt; Hq / Hkv from 1 to 16 (above:
+ *                  UNSUPPORTED).
+ *   learnable_sink, out, lse_new, sink_s  as for sinkattn_decode.  A sequence
+ *                  that sees no key gets out = 0, lse = a_h (-inf without a
+ *                  sink), sink_s = 0.  What masked rows hold, NaN included, does
+ *                  not matter.
+ *   workspace      at least sinkattn_paged_decode_workspace_bytes bytes, any
+ *                  contents; not shared by calls that may overlap.
+ * The work is divided over the GPU from the sequences' lengths on the device, so
+ * a captured call stays balanced when they change.
+ * sinkattn_paged_decode_fp8 -- the same over the 8-bit cache (q, out of type dt). */
+size_t sinkattn_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int D);
+int sinkattn_paged_decode(sinkattn_dtype dt, int Hq, float scale, const void *q,
+                          const sinkattn_paged_cache *cache, int n_sink, int window,
+                          const float *learnable_sink, void *out, float *lse_new, float *sink_s,
+                          void *workspace, size_t workspace_bytes, sinkattn_stream_t stream);
+int sinkattn_paged_decode_fp8(sinkattn_dtype dt, int Hq, float scale, const void *q,
+                              const sinkattn_paged_cache *cache, int n_sink, int window,
+                              const float *learnable_sink, void *out, float *lse_new,
+                              float *sink_s, void *workspace, size_t workspace_bytes,
+                              sinkattn_stream_t stream);
+
 /* ---- profiling hook ---------------------------------------------------------
  * Records CUDA events around the main kernel of later calls, on the stream
  * that kernel is launched on, so a caller can time that kernel alone (the

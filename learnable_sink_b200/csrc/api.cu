@@ -4,6 +4,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "paged.cuh"
 
 // First error any kernel of this library recorded on this device.
 __device__ int g_sinkattn_status;
@@ -437,6 +438,166 @@ int sinkattn_decode_fp8(int B, int Hq, int Hkv, int D, float scale, const void* 
   return launch_decode_fp8(x, reinterpret_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+bool fits_int(long long v) { return v <= INT_MAX; }
+
+// Checks shared by the paged entry points, and the kernels' view of the cache.
+int paged_view(const sinkattn_paged_cache* c, sinkattn_dtype dt, int Hq, bool fp8, PagedView* v) {
+  if (!c) return SINKATTN_ERR_INVALID_ARG;
+  if (dt != SINKATTN_BF16 && dt != SINKATTN_FP16)
+    return dt == SINKATTN_FP32 ? SINKATTN_ERR_UNSUPPORTED : SINKATTN_ERR_INVALID_ARG;
+  if (c->B < 1 || c->B > 65535 || c->Hkv < 1 || c->Hkv > 65535 || (c->D != 64 && c->D != 128))
+    return SINKATTN_ERR_INVALID_ARG;
+  if (Hq < 1 || Hq % c->Hkv != 0) return SINKATTN_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->max_pages < 1) return SINKATTN_ERR_INVALID_ARG;
+  int log2 = 4;
+  while (log2 < 7 && (1 << log2) != c->page_size) ++log2;
+  if ((1 << log2) != c->page_size) return SINKATTN_ERR_UNSUPPORTED;
+  // rows of the pool and positions of a sequence are counted in 32 bits
+  if (!fits_int((long long)c->n_pages * c->page_size) ||
+      !fits_int((long long)c->n_pages * c->page_size * c->Hkv) ||
+      !fits_int((long long)c->max_pages * c->page_size) || !fits_int((long long)c->B * c->Hkv))
+    return SINKATTN_ERR_INVALID_ARG;
+  if (!c->k_pages || !c->v_pages || !c->block_table || !c->cache_seqlens)
+    return SINKATTN_ERR_INVALID_ARG;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return SINKATTN_ERR_INVALID_ARG;
+  if (fp8 != (c->k_scale != nullptr) || fp8 != (c->v_scale != nullptr))
+    return SINKATTN_ERR_INVALID_ARG;
+  if (!device_is_sm100()) return SINKATTN_ERR_UNSUPPORTED;
+  v->k_pages = c->k_pages;
+  v->v_pages = c->v_pages;
+  v->k_scale = c->k_scale;
+  v->v_scale = c->v_scale;
+  v->table = c->block_table;
+  v->seqlens = c->cache_seqlens;
+  v->B = c->B;
+  v->n_pages = c->n_pages;
+  v->page_size = c->page_size;
+  v->page_log2 = log2;
+  v->max_pages = c->max_pages;
+  v->Hkv = c->Hkv;
+  v->status = status_word();
+  return v->status ? SINKATTN_OK : SINKATTN_ERR_CUDA;
+}
+
+bool stride_ok(long long stride, long long row) { return stride >= row && stride % 8 == 0; }
+
+int paged_append(bool fp8, sinkattn_dtype dt, int T, int Hq, const sinkattn_paged_cache* cache,
+                 const void* k, long long k_stride, const void* v, long long v_stride,
+                 const void* q, long long q_stride, const int32_t* cu_new, const float* rope,
+                 int rot_dim, int n_pos, int interleaved, void* q_out, void* k_out,
+                 sinkattn_stream_t stream) {
+  PagedAppendProblem p{};
+  if (!cache || T < 0 || (T > 0 && (!k || !v)) || !aligned16(k) || !aligned16(v))
+    return SINKATTN_ERR_INVALID_ARG;
+  if (!q != !q_out || (q && (!aligned16(q) || !aligned16(q_out)))) return SINKATTN_ERR_INVALID_ARG;
+  if (k_out && !aligned16(k_out)) return SINKATTN_ERR_INVALID_ARG;
+  const long long kv_row = (long long)cache->Hkv * cache->D;
+  if (!stride_ok(k_stride, kv_row) || !stride_ok(v_stride, kv_row) ||
+      (q && !stride_ok(q_stride, (long long)Hq * cache->D)))
+    return SINKATTN_ERR_INVALID_ARG;
+  if (!cu_new && T != cache->B) return SINKATTN_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return SINKATTN_ERR_INVALID_ARG;
+  if (rope && (!aligned16(rope) || rot_dim < 16 || rot_dim > cache->D || rot_dim % 16 != 0 ||
+               n_pos < 1))
+    return SINKATTN_ERR_INVALID_ARG;
+  const int rc = paged_view(cache, dt, q ? Hq : cache->Hkv, fp8, &p.c);
+  if (rc != SINKATTN_OK) return rc;
+  if (T == 0) return SINKATTN_OK;
+  p.dt = dt;
+  p.T = T;
+  p.Hq = Hq;
+  p.D = cache->D;
+  p.rot = rope ? rot_dim : 0;
+  p.n_pos = n_pos;
+  p.interleaved = interleaved;
+  p.k = k;
+  p.v = v;
+  p.q = q;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_stride = q_stride;
+  p.cu = cu_new;
+  p.rope = rope;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return fp8 ? launch_paged_append_fp8(p, s) : launch_paged_append(p, s);
+}
+
+int paged_decode(bool fp8, sinkattn_dtype dt, int Hq, float scale, const void* q,
+                 const sinkattn_paged_cache* cache, int n_sink, int window, const float* sink,
+                 void* out, float* lse_new, float* sink_s, void* workspace,
+                 size_t workspace_bytes, sinkattn_stream_t stream) {
+  PagedDecodeProblem p{};
+  if (!q || !out || !lse_new || !workspace || n_sink < 0 || window < 0)
+    return SINKATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return SINKATTN_ERR_INVALID_ARG;
+  const int rc = paged_view(cache, dt, Hq, fp8, &p.c);
+  if (rc != SINKATTN_OK) return rc;
+  if (Hq / cache->Hkv > kPagedMaxGroup) return SINKATTN_ERR_UNSUPPORTED;
+  if (workspace_bytes < sinkattn_paged_decode_workspace_bytes(cache->B, Hq, cache->Hkv, cache->D))
+    return SINKATTN_ERR_WORKSPACE;
+  p.dt = dt;
+  p.Hq = Hq;
+  p.D = cache->D;
+  p.n_sink = n_sink;
+  p.window = window;
+  p.fp8 = fp8;
+  p.scale = scale;
+  p.q = q;
+  p.sink = sink;
+  p.out = out;
+  p.lse = lse_new;
+  p.sink_s = sink_s;
+  p.part = static_cast<float*>(workspace);
+  return launch_paged_decode(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+int sinkattn_paged_append(sinkattn_dtype dt, int T, int Hq, const sinkattn_paged_cache* cache,
+                          const void* k, long long k_stride, const void* v, long long v_stride,
+                          const void* q, long long q_stride, const int32_t* cu_new,
+                          const float* rope, int rot_dim, int n_pos, int interleaved, void* q_out,
+                          void* k_out, sinkattn_stream_t stream) {
+  return paged_append(false, dt, T, Hq, cache, k, k_stride, v, v_stride, q, q_stride, cu_new, rope,
+                      rot_dim, n_pos, interleaved, q_out, k_out, stream);
+}
+
+int sinkattn_paged_append_fp8(sinkattn_dtype dt, int T, int Hq, const sinkattn_paged_cache* cache,
+                              const void* k, long long k_stride, const void* v,
+                              long long v_stride, const void* q, long long q_stride,
+                              const int32_t* cu_new, const float* rope, int rot_dim, int n_pos,
+                              int interleaved, void* q_out, void* k_out,
+                              sinkattn_stream_t stream) {
+  return paged_append(true, dt, T, Hq, cache, k, k_stride, v, v_stride, q, q_stride, cu_new, rope,
+                      rot_dim, n_pos, interleaved, q_out, k_out, stream);
+}
+
+size_t sinkattn_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int D) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
+  return round_up(sizeof(float) * paged_decode_part_floats(B, Hq, Hkv, D, sm_count()));
+}
+
+int sinkattn_paged_decode(sinkattn_dtype dt, int Hq, float scale, const void* q,
+                          const sinkattn_paged_cache* cache, int n_sink, int window,
+                          const float* learnable_sink, void* out, float* lse_new, float* sink_s,
+                          void* workspace, size_t workspace_bytes, sinkattn_stream_t stream) {
+  return paged_decode(false, dt, Hq, scale, q, cache, n_sink, window, learnable_sink, out, lse_new,
+                      sink_s, workspace, workspace_bytes, stream);
+}
+
+int sinkattn_paged_decode_fp8(sinkattn_dtype dt, int Hq, float scale, const void* q,
+                              const sinkattn_paged_cache* cache, int n_sink, int window,
+                              const float* learnable_sink, void* out, float* lse_new,
+                              float* sink_s, void* workspace, size_t workspace_bytes,
+                              sinkattn_stream_t stream) {
+  return paged_decode(true, dt, Hq, scale, q, cache, n_sink, window, learnable_sink, out, lse_new,
+                      sink_s, workspace, workspace_bytes, stream);
+}
+
 int sinkattn_set_kernel_events(int which, void* start, void* stop) {
   if (which < 0 || which > 3 || ((start == nullptr) != (stop == nullptr)))
     return SINKATTN_ERR_INVALID_ARG;
@@ -478,7 +639,7 @@ const char* sinkattn_error_string(int code) {
     case SINKATTN_ERR_CUDA: return "CUDA call failed";
     case SINKATTN_ERR_WORKSPACE: return "workspace or plan buffer too small";
     case SINKATTN_ERR_TIMEOUT: return "device barrier wait timed out";
-    case SINKATTN_ERR_BOUNDS: return "index out of range (cu_seqlens or block_indices)";
+    case SINKATTN_ERR_BOUNDS: return "index out of range (cu_seqlens, block_indices, block_table or positions)";
     case SINKATTN_ERR_PLAN: return "plan does not match the problem";
     default: return "unknown error";
   }

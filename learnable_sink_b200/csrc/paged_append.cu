@@ -1,0 +1,431 @@
+// Appending keys and values to a paged cache, the position rotation applied on
+// the way.
+//
+// A token's position is p = cache_seqlens[b] - n_b + i (the i-th of the n_b new
+// tokens of sequence b; cache_seqlens counts them).  With c_i, s_i the cosine
+// and sine of the position's i-th angle (a float32 table [n_pos, rot]: cosines,
+// then sines), the pair (a, b) of a key or query becomes
+//   a' = a c - b s,   b' = b c + a s,
+// pairs being elements (i, i + rot/2), or (2i, 2i + 1) when interleaved; the
+// elements past rot are copied.  16-bit results are rounded once, from float32.
+//
+// 8-bit cache: a block (page, KV head) holds E4M3 codes of value / s.  s is a
+// power of two, the smallest 2^e (e >= -126) with amax <= 448 2^e over the
+// finite magnitudes written to the block, 0 while they are all 0.  A power of
+// two makes the product code * s exact in 16 bits, and moving a block's earlier
+// codes to a larger scale exact but for codes that become subnormal.
+#include <cuda_fp8.h>
+
+#include "internal.h"
+#include "paged.cuh"
+
+namespace sk {
+
+namespace {
+
+// Sequence of packed token t: the last b with cu[b] <= t (32-way search by the
+// lanes of a warp: one load a step for up to 32 sequences).
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int t, int lane) {
+  int lo = 0, n = B;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;
+    const bool le = i < n && __ldg(cu + lo + i) <= t;
+    const int hit = __popc(__ballot_sync(0xffffffffu, le));
+    const int skip = hit > 0 ? (hit - 1) * step : 0;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  return lo;
+}
+
+// Page id of position `pos` of sequence b, or -1 with the status set when the
+// table's row does not reach it or names no page of the pool.
+__device__ __forceinline__ int page_of(const PagedView& c, int b, int page_idx) {
+  int id = -1;
+  if (page_idx >= 0 && page_idx < c.max_pages)
+    id = __ldg(c.table + (long long)b * c.max_pages + page_idx);
+  if (id < 0 || id >= c.n_pages) {
+    set_status(c.status, SINKATTN_ERR_BOUNDS);
+    return -1;
+  }
+  return id;
+}
+
+// The two 8-element column chunks that a thread owns in every row, so that each
+// rotated pair lies in one thread: chunk j of the row's D/16.
+struct Chunks {
+  int a, b;       // first columns
+  bool rotated;
+};
+__device__ __forceinline__ Chunks row_chunks(int j, int rot, int interleaved) {
+  Chunks c;
+  c.rotated = 16 * j < rot;
+  const bool split = c.rotated && !interleaved;
+  c.a = split ? 8 * j : 16 * j;
+  c.b = split ? rot / 2 + 8 * j : 16 * j + 8;
+  return c;
+}
+
+// cosines and sines [8 j, 8 j + 8) of a position: either pairing's angles of
+// the thread's sixteen elements
+struct Angles {
+  float c[8], s[8];
+};
+__device__ __forceinline__ void load_angles(Angles& t, const float* rope, long long pos, int rot,
+                                            int j) {
+  const float4* c = reinterpret_cast<const float4*>(rope + pos * rot + 8 * j);
+  const float4* s = reinterpret_cast<const float4*>(rope + pos * rot + rot / 2 + 8 * j);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 x = __ldg(c + i), y = __ldg(s + i);
+    t.c[4 * i] = x.x; t.c[4 * i + 1] = x.y; t.c[4 * i + 2] = x.z; t.c[4 * i + 3] = x.w;
+    t.s[4 * i] = y.x; t.s[4 * i + 1] = y.y; t.s[4 * i + 2] = y.z; t.s[4 * i + 3] = y.w;
+  }
+}
+
+template <class E>
+__device__ __forceinline__ void widen8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = E::widen(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <class E>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(E::pack(x[0], x[1]), E::pack(x[2], x[3]), E::pack(x[4], x[5]),
+                    E::pack(x[6], x[7]));
+}
+
+__device__ __forceinline__ void rotate16(float (&a)[8], float (&b)[8], const Angles& t,
+                                         int interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
+      a[2 * i] = a0 * t.c[i] - a1 * t.s[i];
+      a[2 * i + 1] = a1 * t.c[i] + a0 * t.s[i];
+      b[2 * i] = b0 * t.c[4 + i] - b1 * t.s[4 + i];
+      b[2 * i + 1] = b1 * t.c[4 + i] + b0 * t.s[4 + i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = a[i], y = b[i];
+      a[i] = x * t.c[i] - y * t.s[i];
+      b[i] = y * t.c[i] + x * t.s[i];
+    }
+  }
+}
+
+// Where a packed token goes.
+struct Place {
+  int b, pos;  // b < 0: no sequence of the call has it, or it is out of bounds
+};
+__device__ __forceinline__ Place place_token(const PagedAppendProblem& p, int t, int lane) {
+  Place r{-1, 0};
+  if (p.cu) {
+    const int b = find_sequence(p.cu, p.c.B, t, lane);
+    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
+    if (t < c0 || t >= c1) return r;  // rows behind the last sequence
+    r.pos = __ldg(p.c.seqlens + b) - (c1 - t);
+    r.b = b;
+  } else {
+    const int n = __ldg(p.c.seqlens + t);
+    if (n <= 0) return r;  // a slot without a new token
+    r.pos = n - 1;
+    r.b = t;
+  }
+  if (r.pos < 0 || (p.rope && r.pos >= p.n_pos)) {
+    set_status(p.c.status, SINKATTN_ERR_BOUNDS);
+    r.b = -1;
+  }
+  return r;
+}
+
+// Copy or rotate the 16-bit rows of one token: rows [0, Hq) are its queries,
+// then Hkv keys, then Hkv values (only the queries when kv = false).  Thread
+// (j, g) of the token's D/16 x NG takes chunk pair j of rows g, g + NG, ...;
+// its angles are loaded once for all of them, and four rows are in flight.
+template <class E, int D>
+__device__ __forceinline__ void token_rows(const PagedAppendProblem& p, int t, int j, int g,
+                                           int NG, bool kv, int lane) {
+  using T = typename E::T;
+  const int Hq = p.q ? p.Hq : 0, Hkv = p.c.Hkv;
+  const int rows = kv ? Hq + 2 * Hkv : Hq;
+  const Place pl = place_token(p, t, lane);
+  if (pl.b < 0) return;
+  T* kdst = nullptr;
+  T* vdst = nullptr;
+  if (kv) {
+    const int page = page_of(p.c, pl.b, pl.pos >> p.c.page_log2);
+    if (page < 0) return;
+    const long long at =
+        (((long long)page * Hkv << p.c.page_log2) + (pl.pos & (p.c.page_size - 1))) * D;
+    kdst = static_cast<T*>(p.c.k_pages) + at;
+    vdst = static_cast<T*>(p.c.v_pages) + at;
+  }
+  const long long head_step = (long long)D << p.c.page_log2;
+  const Chunks ch = row_chunks(j, p.rot, p.interleaved);
+  Angles an;
+  if (ch.rotated) load_angles(an, p.rope, pl.pos, p.rot, j);
+  const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
+  const T* k = static_cast<const T*>(p.k) + t * p.k_stride;
+  const T* v = static_cast<const T*>(p.v) + t * p.v_stride;
+  T* qo = static_cast<T*>(p.q_out) + (long long)t * p.Hq * D;
+  T* ko = p.k_out && kv ? static_cast<T*>(p.k_out) + (long long)t * Hkv * D : nullptr;
+  constexpr int U = 4;
+  for (int r0 = g; r0 < rows; r0 += U * NG) {
+    uint4 xa[U], xb[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * NG;
+      if (r < rows) {
+        const T* src = r < Hq ? q + r * D : r < Hq + Hkv ? k + (r - Hq) * D : v + (r - Hq - Hkv) * D;
+        xa[u] = *reinterpret_cast<const uint4*>(src + ch.a);
+        xb[u] = *reinterpret_cast<const uint4*>(src + ch.b);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * NG;
+      if (r >= rows) break;
+      if (ch.rotated && r < Hq + Hkv) {
+        float a[8], b[8];
+        widen8<E>(xa[u], a);
+        widen8<E>(xb[u], b);
+        rotate16(a, b, an, p.interleaved);
+        xa[u] = pack8<E>(a);
+        xb[u] = pack8<E>(b);
+      }
+      T* dst = r < Hq ? qo + r * D
+                      : r < Hq + Hkv ? kdst + (r - Hq) * head_step : vdst + (r - Hq - Hkv) * head_step;
+      *reinterpret_cast<uint4*>(dst + ch.a) = xa[u];
+      *reinterpret_cast<uint4*>(dst + ch.b) = xb[u];
+      if (ko && r >= Hq && r < Hq + Hkv) {
+        *reinterpret_cast<uint4*>(ko + (r - Hq) * D + ch.a) = xa[u];
+        *reinterpret_cast<uint4*>(ko + (r - Hq) * D + ch.b) = xb[u];
+      }
+    }
+  }
+}
+
+constexpr int kAppendThreads = 256;
+
+template <class E, int D>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedAppendProblem p, int NG) {
+  constexpr int NC = D / 16;
+  const int per_token = NC * NG;  // a multiple of 32: a warp stays in one token
+  const long long t =
+      (long long)blockIdx.x * (kAppendThreads / per_token) + threadIdx.x / per_token;
+  if (t >= p.T) return;
+  const int i = threadIdx.x % per_token;
+  token_rows<E, D>(p, (int)t, i % NC, i / NC, NG, true, threadIdx.x & 31);
+}
+
+// ---------------------------------------------------------------- 8-bit cache
+// The smallest power of two s >= 2^-126 with amax <= 448 s (448 = 1.75 2^8),
+// 0 for amax = 0.
+__device__ __forceinline__ float block_scale(float amax) {
+  if (!(amax > 0.f)) return 0.f;
+  const uint32_t u = __float_as_uint(amax);
+  int e = int(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // biased exponent of s
+  if (e < 1) e = 1;
+  return __uint_as_float(uint32_t(e) << 23);
+}
+__device__ __forceinline__ float finite_abs(float x) {
+  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
+  return u < 0x7f800000u ? __uint_as_float(u) : 0.f;
+}
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return (lo & 0xffffu) | (hi << 16);
+}
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float m) {
+  return make_uint2(encode4(x[0] * m, x[1] * m, x[2] * m, x[3] * m),
+                    encode4(x[4] * m, x[5] * m, x[6] * m, x[7] * m));
+}
+__device__ __forceinline__ float2 decode2(uint32_t two) {
+  const __half2_raw h =
+      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu), __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+__device__ __forceinline__ uint32_t rescale4(uint32_t codes, float m) {
+  const float2 a = decode2(codes), b = decode2(codes >> 16);
+  return encode4(a.x * m, a.y * m, b.x * m, b.y * m);
+}
+
+// One block of the grid per touched (page, KV head): warps [0, page/16) take its
+// key rows, sixteen each, the other half of the warps its value rows.  The new
+// rows are read once and stay in registers between the block's amax and the
+// encoding.  Blocks behind the pages' rotate the queries.
+//
+// The pages that a sequence touches need no prefix sum: n tokens touch at most
+// n/page + 2 pages (rounded down), so sequence b owns items
+// [cu[b]/page + 2b, cu[b + 1]/page + 2(b + 1)) and the rest of them are idle.
+template <class E, int D>
+__global__ void __launch_bounds__(512) paged_append_fp8_kernel(PagedAppendProblem p, int items,
+                                                              unsigned page_blocks, int NG) {
+  using T = typename E::T;
+  constexpr int NC = D / 16;         // threads per row
+  constexpr int RPP = 32 / NC;       // rows per pass of a warp
+  constexpr int PASSES = 16 / RPP;
+  __shared__ float s_max[16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x >= page_blocks) {
+    const int per_token = NC * NG;
+    const long long t = (long long)(blockIdx.x - page_blocks) * (blockDim.x / per_token) +
+                        threadIdx.x / per_token;
+    const int i = threadIdx.x % per_token;
+    if (t < p.T && threadIdx.x / per_token < blockDim.x / per_token)
+      token_rows<E, D>(p, (int)t, i % NC, i / NC, NG, false, lane);
+    return;
+  }
+  const PagedView& c = p.c;
+  const int item = blockIdx.x / c.Hkv, h = blockIdx.x % c.Hkv;
+  // the sequence, and the new tokens [t0, t1) that fall in the item's page
+  int b, c0, c1;
+  if (p.cu) {
+    int lo = 0, n = c.B;
+    while (n > 1) {
+      const int step = (n + 31) / 32, i = lane * step;
+      const bool le = i < n && (__ldg(p.cu + lo + i) >> c.page_log2) + 2 * (lo + i) <= item;
+      const int hit = __popc(__ballot_sync(0xffffffffu, le));
+      const int skip = hit > 0 ? (hit - 1) * step : 0;
+      lo += skip;
+      n = min(step, n - skip);
+    }
+    b = lo;
+    c0 = __ldg(p.cu + b);
+    c1 = __ldg(p.cu + b + 1);
+  } else {
+    b = item;
+    c0 = b;
+    c1 = b + 1;
+  }
+  const int n_new = c1 - c0;
+  const int len = __ldg(c.seqlens + b);
+  if (n_new <= 0 || (!p.cu && len <= 0)) return;
+  const int start = len - n_new;  // position of token c0
+  const int end = p.rope ? min(len, p.n_pos) : len;
+  if ((start < 0 || end < len) && threadIdx.x == 0) set_status(c.status, SINKATTN_ERR_BOUNDS);
+  const int first = start >> c.page_log2;  // page of the sequence's first new token
+  const int page_idx = first + (p.cu ? item - ((c0 >> c.page_log2) + 2 * b) : 0);
+  const int pos0 = page_idx << c.page_log2;  // position of the page's row 0
+  const int r0 = max(start - pos0, 0), r1 = min(end - pos0, c.page_size);
+  if (page_idx < max(first, 0) || r0 >= r1) return;
+  const int page = page_of(c, b, page_idx);
+  if (page < 0) return;
+
+  const int half = blockDim.x >> 6;  // warps of each of K and V
+  const bool is_v = warp >= half;
+  const int row_base = (is_v ? warp - half : warp) * 16;
+  const int j = lane % NC, sub = lane / NC;
+  const Chunks ch = is_v ? Chunks{16 * j, 16 * j + 8, false} : row_chunks(j, p.rot, p.interleaved);
+  const T* src = is_v ? static_cast<const T*>(p.v) : static_cast<const T*>(p.k);
+  const long long tstride = is_v ? p.v_stride : p.k_stride;
+  float xa[PASSES][8], xb[PASSES][8];
+  float amax = 0.f;
+#pragma unroll
+  for (int u = 0; u < PASSES; ++u) {
+    const int r = row_base + u * RPP + sub;
+    const long long t = (long long)c0 + (pos0 + r - start);
+    const bool on = r >= r0 && r < r1 && t >= 0 && t < p.T;
+    uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
+    if (on) {
+      ua = *reinterpret_cast<const uint4*>(src + t * tstride + h * D + ch.a);
+      ub = *reinterpret_cast<const uint4*>(src + t * tstride + h * D + ch.b);
+    }
+    widen8<E>(ua, xa[u]);
+    widen8<E>(ub, xb[u]);
+    if (on && ch.rotated) {
+      Angles an;
+      load_angles(an, p.rope, pos0 + r, p.rot, j);
+      rotate16(xa[u], xb[u], an, p.interleaved);
+    }
+    if (on && !is_v && p.k_out) {
+      T* ko = static_cast<T*>(p.k_out) + (t * c.Hkv + h) * D;
+      *reinterpret_cast<uint4*>(ko + ch.a) = pack8<E>(xa[u]);
+      *reinterpret_cast<uint4*>(ko + ch.b) = pack8<E>(xb[u]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(finite_abs(xa[u][i]), finite_abs(xb[u][i])));
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (lane == 0) s_max[warp] = amax;
+  float* scale_at = (is_v ? c.v_scale : c.k_scale) + (long long)page * c.Hkv + h;
+  const float s_old = r0 > 0 ? *scale_at : 0.f;
+  __syncthreads();
+  amax = 0.f;
+  for (int w = 0; w < half; ++w) amax = fmaxf(amax, s_max[(is_v ? half : 0) + w]);
+  const float s = fmaxf(block_scale(amax), s_old);
+  uint8_t* dst = static_cast<uint8_t*>(is_v ? c.v_pages : c.k_pages) +
+                 (((long long)page * c.Hkv + h) << c.page_log2) * D;
+  // where every value is 0 (or not finite) any factor will do
+  const float inv = s > 0.f ? __frcp_rn(s) : 1.f;
+  const bool grow = s > s_old && r0 > 0;
+  const float ratio = s_old * inv;
+#pragma unroll
+  for (int u = 0; u < PASSES; ++u) {
+    const int r = row_base + u * RPP + sub;
+    uint2* da = reinterpret_cast<uint2*>(dst + (long long)r * D + ch.a);
+    uint2* db = reinterpret_cast<uint2*>(dst + (long long)r * D + ch.b);
+    if (r >= r0 && r < r1) {
+      *da = encode8(xa[u], inv);
+      *db = encode8(xb[u], inv);
+    } else if (grow && r < r0) {
+      const uint2 a = *da, bq = *db;
+      *da = make_uint2(rescale4(a.x, ratio), rescale4(a.y, ratio));
+      *db = make_uint2(rescale4(bq.x, ratio), rescale4(bq.y, ratio));
+    }
+  }
+  if (lane == 0 && row_base == 0) *scale_at = s;
+}
+
+// Row groups of a token's threads: eight leave a thread several rows, whose
+// loads overlap and share its angles; with few tokens the whole block of 256
+// threads takes one token, for latency.
+int row_groups(int T, int D) { return T < 4 * 148 ? kAppendThreads / (D / 16) : 8; }
+
+template <class E, int D>
+int append_typed(const PagedAppendProblem& p, cudaStream_t stream) {
+  const int NG = row_groups(p.T, D), per_token = D / 16 * NG;
+  const long long blocks = ((long long)p.T * per_token + kAppendThreads - 1) / kAppendThreads;
+  if (blocks > 0x7fffffffLL) return SINKATTN_ERR_INVALID_ARG;
+  paged_append_kernel<E, D><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p, NG);
+  return cudaGetLastError() == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA;
+}
+
+template <class E, int D>
+int append_fp8_typed(const PagedAppendProblem& p, cudaStream_t stream) {
+  const int threads = p.c.page_size / 16 * 64;
+  const long long items = p.cu ? p.T / p.c.page_size + 2LL * p.c.B : p.c.B;
+  const long long pages = items * p.c.Hkv;
+  const int NG = 128 / D * 8;  // 64 threads a token: every block size holds whole tokens
+  const int tokens = threads / (D / 16 * NG);
+  const long long q_blocks = p.q ? (p.T + tokens - 1) / tokens : 0;
+  if (pages + q_blocks > 0x7fffffffLL) return SINKATTN_ERR_INVALID_ARG;
+  paged_append_fp8_kernel<E, D><<<(unsigned)(pages + q_blocks), threads, 0, stream>>>(
+      p, (int)items, (unsigned)pages, NG);
+  return cudaGetLastError() == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_paged_append(const PagedAppendProblem& p, cudaStream_t s) {
+  if (p.dt == SINKATTN_FP16)
+    return p.D == 128 ? append_typed<ElemF16, 128>(p, s) : append_typed<ElemF16, 64>(p, s);
+  return p.D == 128 ? append_typed<ElemBf16, 128>(p, s) : append_typed<ElemBf16, 64>(p, s);
+}
+int launch_paged_append_fp8(const PagedAppendProblem& p, cudaStream_t s) {
+  if (p.dt == SINKATTN_FP16)
+    return p.D == 128 ? append_fp8_typed<ElemF16, 128>(p, s) : append_fp8_typed<ElemF16, 64>(p, s);
+  return p.D == 128 ? append_fp8_typed<ElemBf16, 128>(p, s) : append_fp8_typed<ElemBf16, 64>(p, s);
+}
+
+}  // namespace sk

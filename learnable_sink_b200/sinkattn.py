@@ -38,6 +38,14 @@ class CMask(_c.Structure):
                 ("block_k", _c.c_int32), ("max_blocks", _c.c_int32)]
 
 
+class CPagedCache(_c.Structure):
+    """Mirror of ``sinkattn_paged_cache``."""
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("k_scale", _vp), ("v_scale", _vp),
+                ("block_table", _vp), ("cache_seqlens", _vp), ("B", _c.c_int32),
+                ("n_pages", _c.c_int32), ("page_size", _c.c_int32), ("max_pages", _c.c_int32),
+                ("Hkv", _c.c_int32), ("D", _c.c_int32)]
+
+
 class SinkAttnError(RuntimeError):
     def __init__(self, fn, code, detail=None):
         msg = f"{fn} failed: {ERR_NAMES.get(code, code)} ({error_string(code)})"
@@ -89,6 +97,15 @@ def lib():
         L.sinkattn_cache_append.argtypes = [_i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]
         L.sinkattn_cache_fill.argtypes = [_i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp,
                                           _vp, _vp]
+        P, ll = _c.POINTER(CPagedCache), _c.c_longlong
+        append = [_i, _i, _i, P, _vp, ll, _vp, ll, _vp, ll, _vp, _vp, _i, _i, _i, _vp, _vp, _vp]
+        L.sinkattn_paged_append.argtypes = append
+        L.sinkattn_paged_append_fp8.argtypes = append
+        L.sinkattn_paged_decode_workspace_bytes.restype = _sz
+        L.sinkattn_paged_decode_workspace_bytes.argtypes = [_i, _i, _i, _i]
+        paged = [_i, _i, _c.c_float, _vp, P, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+        L.sinkattn_paged_decode.argtypes = paged
+        L.sinkattn_paged_decode_fp8.argtypes = paged
         L.sinkattn_set_kernel_events.argtypes = [_i, _vp, _vp]
         L.sinkattn_selftest_timeout.argtypes = [_vp]
         L.sinkattn_get_status.argtypes = [_vp]
@@ -484,6 +501,211 @@ def cache_fill(k, v, cu_seqlens, k_cache, v_cache, n_sink: int, window: int,
     _check("sinkattn_cache_fill", lib().sinkattn_cache_fill(
         _dt(k), n_seq, T, Hkv, D, int(n_sink), int(window), _ptr(cu_seqlens), _ptr(k), _ptr(v),
         _ptr(k_cache), _ptr(v_cache), _ptr(cache_seqlens_out), _stream(stream)))
+
+
+class PagedCache:
+    """A paged K/V cache (see ``sinkattn_paged_cache``): pools ``k_pages`` /
+    ``v_pages`` [n_pages, Hkv, page_size, D] in bfloat16 or float16, or E4M3
+    codes (torch.float8_e4m3fn or uint8) with float32 scales ``k_scale`` /
+    ``v_scale`` [n_pages, Hkv]; ``block_table`` int32 [B, max_pages] and
+    ``cache_seqlens`` int32 [B], which counts a call's new tokens.  The tensors
+    are checked once, here, and kept; their contents may change between calls."""
+
+    __slots__ = ("k_pages", "v_pages", "block_table", "cache_seqlens", "k_scale", "v_scale",
+                 "device", "B", "Hkv", "D", "_c", "_ref")
+
+    def __init__(self, k_pages, v_pages, block_table, cache_seqlens, k_scale=None, v_scale=None):
+        fn = "PagedCache"
+        _want(fn, k_pages.dim() == 4, "pages must be [n_pages, Hkv, page_size, D]")
+        _same_type(fn, k_pages, v_pages=v_pages)
+        _shape(fn, "v_pages", v_pages, k_pages.shape)
+        n_pages, Hkv, page_size, D = k_pages.shape
+        coded = k_pages.element_size() == 1
+        if coded:
+            _want(fn, k_pages.dtype in (torch.float8_e4m3fn, torch.uint8),
+                  f"pages are {k_pages.dtype}, expected float8_e4m3fn or uint8 codes")
+            _want(fn, k_scale is not None and v_scale is not None, "8-bit pages need scales")
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                _shape(fn, name, t, (n_pages, Hkv), torch.float32)
+        else:
+            _want(fn, k_pages.dtype in (torch.bfloat16, torch.float16),
+                  f"pages are {k_pages.dtype}, expected bfloat16, float16 or 8-bit codes")
+            _want(fn, k_scale is None and v_scale is None, "scales go with 8-bit pages")
+        _want(fn, page_size in (16, 32, 64, 128), f"page_size {page_size}: 16, 32, 64 or 128")
+        _want(fn, D in (64, 128), f"D {D}: 64 or 128")
+        _want(fn, block_table.dim() == 2 and block_table.dtype == torch.int32
+              and block_table.numel() > 0, "block_table must be int32 [B, max_pages]")
+        B, max_pages = block_table.shape
+        _shape(fn, "cache_seqlens", cache_seqlens, (B,), torch.int32)
+        ts = (k_pages, v_pages, block_table, cache_seqlens, k_scale, v_scale)
+        _contig(*ts)
+        _one_device(fn, *ts)
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.block_table, self.cache_seqlens = block_table, cache_seqlens
+        self.device, self.B, self.Hkv, self.D = k_pages.device, B, Hkv, D
+        self._c = CPagedCache(k_pages.data_ptr(), v_pages.data_ptr(),
+                              None if k_scale is None else k_scale.data_ptr(),
+                              None if v_scale is None else v_scale.data_ptr(),
+                              block_table.data_ptr(), cache_seqlens.data_ptr(), B, n_pages,
+                              page_size, max_pages, Hkv, D)
+        self._ref = _c.byref(self._c)
+
+
+def _one_device(fn, *ts):
+    dev = ts[0].device
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise SinkAttnError(fn, 1, f"tensors on {dev} and {t.device}")
+
+
+def _current(fn, dev):
+    """The library launches on the current device."""
+    if dev.index != torch.cuda.current_device():
+        raise SinkAttnError(fn, 1, f"tensors on {dev}, current device "
+                                   f"cuda:{torch.cuda.current_device()}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _tokens(fn, name, t, shape, dtype, dev):
+    """A packed [T, H, D] input whose tokens may be strided (a view of a fused
+    projection); returns the token stride in elements."""
+    _shape(fn, name, t, shape, dtype)
+    _want(fn, t.device == dev, f"{name} is on {t.device}, the cache on {dev}")
+    _, H, D = shape
+    st = t.stride()
+    if shape[0] <= 1:
+        st = (H * D, st[1], st[2])
+    _want(fn, st[2] == 1 and (H == 1 or st[1] == D), f"{name}: a token's heads must be contiguous")
+    _want(fn, st[0] >= H * D and st[0] % 8 == 0 and t.data_ptr() % 16 == 0,
+          f"{name}: tokens must be 16-byte aligned and not overlap")
+    return st[0]
+
+
+def _paged_append(fn, call, coded, k, v, cache, cu_new, rope, interleaved, q, q_out, k_out, stream):
+    _want(fn, k.dim() == 3, "k must be [T, Hkv, D]")
+    dev, D = cache.device, cache.D
+    dt = k.dtype
+    pages = cache.k_pages.dtype
+    if coded:
+        _want(fn, cache.k_scale is not None, "the cache is not an 8-bit cache")
+    else:
+        _want(fn, pages == dt, f"k is {dt}, the pages {pages}")
+    T = k.shape[0]
+    kv = (T, cache.Hkv, D)
+    ks = _tokens(fn, "k", k, kv, dt, dev)
+    vs = _tokens(fn, "v", v, kv, dt, dev)
+    Hq = qs = 0
+    if q is not None:
+        _want(fn, q.dim() == 3, "q must be [T, Hq, D]")
+        Hq = q.shape[1]
+        qs = _tokens(fn, "q", q, (T, Hq, D), dt, dev)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+    _want(fn, q is not None or q_out is None, "q_out without q")
+    for name, t, shape in (("q_out", q_out, (T, Hq, D)), ("k_out", k_out, kv)):
+        if t is not None:
+            _shape(fn, name, t, shape, dt)
+            _want(fn, t.device == dev and t.is_contiguous(),
+                  f"{name} must be contiguous, on the cache's device")
+    if cu_new is None:
+        _want(fn, T == cache.B, f"{T} tokens for {cache.B} sequences without cu_new")
+    else:
+        _shape(fn, "cu_new", cu_new, (cache.B + 1,), torch.int32)
+        _want(fn, cu_new.device == dev and cu_new.is_contiguous(),
+              "cu_new must be contiguous, on the cache's device")
+    rot = n_pos = 0
+    if rope is not None:
+        _want(fn, rope.dim() == 2 and rope.dtype == torch.float32 and rope.device == dev
+              and rope.is_contiguous(), "rope must be float32 [n_pos, rot_dim] on the cache's device")
+        n_pos, rot = rope.shape
+        _want(fn, n_pos > 0 and rot % 16 == 0 and 16 <= rot <= D,
+              f"rot_dim {rot}: a multiple of 16 up to {D}")
+    _current(fn, dev)
+    _check(fn, call(_dt(k), T, Hq, cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, _addr(q), qs,
+                    _addr(cu_new), _addr(rope), rot, n_pos, 1 if interleaved else 0, _addr(q_out),
+                    _addr(k_out), _stream(stream)))
+    return q_out
+
+
+def paged_append(k, v, cache: PagedCache, cu_new=None, rope=None, interleaved: bool = False,
+                 q=None, q_out=None, k_out=None, stream=None):
+    """Append packed new tokens (k/v [T, Hkv, D], sequences by cu_new int32
+    [B + 1]; without it one token per sequence) as the last positions that
+    cache.cache_seqlens counts, keys rotated by ``rope`` [n_pos, rot_dim]
+    (cosines, then sines; pairs half a rot_dim apart, or neighbours when
+    interleaved).  ``q`` [T, Hq, D] is rotated into q_out, the rotated keys also
+    go to k_out if given.  k, v and q may be views with strided tokens.
+    Returns q_out."""
+    return _paged_append("sinkattn_paged_append", lib().sinkattn_paged_append, False, k, v, cache,
+                         cu_new, rope, interleaved, q, q_out, k_out, stream)
+
+
+def paged_append_fp8(k, v, cache: PagedCache, cu_new=None, rope=None, interleaved: bool = False,
+                     q=None, q_out=None, k_out=None, stream=None):
+    """paged_append into an 8-bit cache: E4M3 codes with a power-of-two scale for
+    each page and KV head, which grows (the page's earlier codes with it) when
+    new rows need it."""
+    return _paged_append("sinkattn_paged_append_fp8", lib().sinkattn_paged_append_fp8, True, k, v,
+                         cache, cu_new, rope, interleaved, q, q_out, k_out, stream)
+
+
+def paged_decode_workspace_bytes(B, Hq, Hkv, D) -> int:
+    return int(lib().sinkattn_paged_decode_workspace_bytes(B, Hq, Hkv, D))
+
+
+def _paged_decode(fn, call, coded, q, cache, sink, n_sink, window, scale, stream, workspace, out,
+                  lse, sink_s):
+    _want(fn, q.dim() == 3, "q must be [B, Hq, D]")
+    B, Hq, D = q.shape
+    dev = cache.device
+    _want(fn, B == cache.B and D == cache.D, f"q {tuple(q.shape)} and the cache disagree on B or D")
+    if coded:
+        _want(fn, cache.k_scale is not None, "the cache is not an 8-bit cache")
+    else:
+        _same_type(fn, q, k_pages=cache.k_pages)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
+    if sink_s is None:
+        sink_s = torch.empty(B, Hq, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(paged_decode_workspace_bytes(B, Hq, cache.Hkv, D), 16),
+                                dtype=torch.uint8, device=dev)
+    _shape(fn, "out", out, q.shape, q.dtype)
+    _shape(fn, "lse", lse, (B, Hq), torch.float32)
+    _shape(fn, "sink_s", sink_s, (B, Hq), torch.float32)
+    _shape(fn, "learnable_sink", sink, (Hq,), torch.float32)
+    _contig(q, sink, out, lse, sink_s, workspace)
+    _one_device(fn, cache.k_pages, q, sink, out, lse, sink_s, workspace)
+    _current(fn, dev)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    _check(fn, call(_dt(q), Hq, scale, q.data_ptr(), cache._ref, int(n_sink), int(window),
+                    _addr(sink), out.data_ptr(), lse.data_ptr(), sink_s.data_ptr(),
+                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                    _stream(stream)))
+    return out, lse, sink_s
+
+
+def paged_decode(q, cache: PagedCache, sink, n_sink: int = 0, window: int = 0,
+                 scale: Optional[float] = None, stream=None, workspace=None, out=None, lse=None,
+                 sink_s=None):
+    """One query token per sequence (q [B, Hq, D]) over a paged 16-bit cache;
+    with window > 0 only the first n_sink and the last ``window`` positions are
+    visible.  Returns (out [B,Hq,D], lse_new [B,Hq], sink_s [B,Hq])."""
+    return _paged_decode("sinkattn_paged_decode", lib().sinkattn_paged_decode, False, q, cache,
+                         sink, n_sink, window, scale, stream, workspace, out, lse, sink_s)
+
+
+def paged_decode_fp8(q, cache: PagedCache, sink, n_sink: int = 0, window: int = 0,
+                     scale: Optional[float] = None, stream=None, workspace=None, out=None,
+                     lse=None, sink_s=None):
+    """paged_decode over an 8-bit cache (q and out bfloat16 or float16)."""
+    return _paged_decode("sinkattn_paged_decode_fp8", lib().sinkattn_paged_decode_fp8, True, q,
+                         cache, sink, n_sink, window, scale, stream, workspace, out, lse, sink_s)
 
 
 KERNEL_FWD, KERNEL_BWD, KERNEL_DECODE, KERNEL_GATE = 0, 1, 2, 3

@@ -344,6 +344,137 @@ def decode_fp8_window(q, k_sink, v_sink, k_win, v_win, k_scale, v_scale, cache_s
     return decode(q, k, v, cache_seqlens, n_sink, window, sink, scale)
 
 
+def rope_table(n_pos, rot_dim, base=10000.0):
+    """Cosines and sines of every position's rot_dim / 2 angles
+    p base^(-2 i / rot_dim), [n_pos, rot_dim] float64 (cosines, then sines)."""
+    a = np.arange(n_pos, dtype=np.float64)[:, None] * base ** (
+        -np.arange(0, rot_dim, 2, dtype=np.float64) / rot_dim)
+    return np.concatenate([np.cos(a), np.sin(a)], axis=1)
+
+
+def rotate(x, positions, rope, interleaved=False):
+    """Rotate the heads of x [n, H, D] to their positions by the table's rows:
+    the pair (a, b) becomes (a c - b s, b c + a s) as the complex product
+    (a + ib)(c + is); pairs are (i, i + R/2), or (2i, 2i + 1)."""
+    y = _f64(x).copy()
+    rope = _f64(rope)
+    R = rope.shape[1]
+    rows = rope[np.asarray(positions, dtype=np.int64)]
+    turn = (rows[:, : R // 2] + 1j * rows[:, R // 2:])[:, None, :]
+    ia = np.arange(0, R, 2) if interleaved else np.arange(R // 2)
+    ib = ia + 1 if interleaved else ia + R // 2
+    z = (y[..., ia] + 1j * y[..., ib]) * turn
+    y[..., ia], y[..., ib] = z.real, z.imag
+    return y
+
+
+def _new_tokens(cu_new, cache_seqlens):
+    """(token, sequence, position) of every packed new token of a call."""
+    lens = np.asarray(cache_seqlens, dtype=np.int64).reshape(-1)
+    for b, n in enumerate(lens):
+        if cu_new is None:
+            if n > 0:
+                yield b, b, int(n) - 1
+            continue
+        c0, c1 = int(cu_new[b]), int(cu_new[b + 1])
+        for t in range(c0, c1):
+            yield t, b, int(n) - (c1 - t)
+
+
+def paged_append(k, v, block_table, cache_seqlens, k_pages, v_pages, cu_new=None):
+    """Write packed new tokens (k, v [T, Hkv, D], already rotated) into copies of
+    the pages [n_pages, Hkv, page, D]: position p of sequence b goes to row
+    p mod page of page block_table[b, p // page]."""
+    kp, vp = _f64(k_pages).copy(), _f64(v_pages).copy()
+    page = kp.shape[2]
+    k, v = _f64(k), _f64(v)
+    table = np.asarray(block_table)
+    for t, b, pos in _new_tokens(cu_new, cache_seqlens):
+        at = table[b, pos // page]
+        kp[at, :, pos % page] = k[t]
+        vp[at, :, pos % page] = v[t]
+    return kp, vp
+
+
+def block_scale(amax):
+    """The smallest power of two s = 2^e, e >= -126, with amax <= 448 s, by
+    trying the exponents upwards; 0 for amax = 0."""
+    if amax == 0:
+        return 0.0
+    e = -126
+    while amax > 448.0 * 2.0 ** e:
+        e += 1
+    return 2.0 ** e
+
+
+def paged_append_fp8(x, block_table, cache_seqlens, codes, scale, cu_new=None):
+    """One of K or V: write x [T, Hkv, D] (already rotated) into copies of the
+    8-bit pages (uint8 codes [n_pages, Hkv, page, D], scales [n_pages, Hkv]).  The
+    rows that a call adds to a block set its scale together; a block with
+    earlier rows keeps the larger scale and has their codes re-encoded."""
+    x, codes, scale = _f64(x), _u8arr(codes).copy(), _f64(scale).copy()
+    page = codes.shape[2]
+    table = np.asarray(block_table)
+    touched = {}
+    for t, b, pos in _new_tokens(cu_new, cache_seqlens):
+        touched.setdefault((int(table[b, pos // page])), []).append((pos % page, t))
+    for at, rows in touched.items():
+        first = min(r for r, _ in rows)
+        for h in range(codes.shape[1]):
+            new = np.stack([x[t, h] for _, t in rows])
+            mag = np.abs(new[np.isfinite(new)])
+            s = block_scale(float(mag.max()) if mag.size else 0.0)
+            if first > 0:
+                old = float(scale[at, h])
+                s = max(s, old)
+                if s > old:
+                    codes[at, h, :first] = fp8_e4m3_encode(
+                        fp8_e4m3_value(codes[at, h, :first]) * old / s)
+            scale[at, h] = s
+            for r, t in rows:
+                codes[at, h, r] = fp8_e4m3_encode(x[t, h] / (s if s > 0 else 1.0))
+    return codes, scale
+
+
+def paged_decode(q, k_pages, v_pages, block_table, cache_seqlens, n_sink, window, sink, scale,
+                 k_scale=None, v_scale=None):
+    """Single-token attention over a paged cache: for every sequence the visible
+    positions are gathered row by row and an augmented softmax (the sink an
+    extra column of value 0) is taken over them.  8-bit pages: uint8 codes and
+    scales [n_pages, Hkv].  Returns (out, lse_new, sink_s)."""
+    q = _f64(q)
+    sink = None if sink is None else _f64(sink)
+    coded = k_scale is not None
+    kp, vp = (fp8_e4m3_value(_u8arr(t)) if coded else _f64(t) for t in (k_pages, v_pages))
+    if coded:
+        ks, vs = _f64(k_scale), _f64(v_scale)
+    table = np.asarray(block_table)
+    B, Hq, D = q.shape
+    Hkv, page = kp.shape[1], kp.shape[2]
+    out, lse, ss = np.zeros((B, Hq, D)), np.full((B, Hq), -np.inf), np.zeros((B, Hq))
+    for b, n in enumerate(np.asarray(cache_seqlens, dtype=np.int64).reshape(-1)):
+        pos = np.array([j for j in range(int(n))
+                        if window <= 0 or j < n_sink or j >= n - window], dtype=np.int64)
+        at, row = table[b, pos // page], pos % page
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            k, v = kp[at, g, row], vp[at, g, row]
+            if coded:
+                k, v = k * ks[at, g][:, None], v * vs[at, g][:, None]
+            x = scale * (k @ q[b, h])
+            m = max([x.max()] if pos.size else [], default=-np.inf)
+            if sink is not None:
+                m = max(m, sink[h])
+            if m == -np.inf:
+                continue
+            e = np.exp(x - m)
+            den = e.sum() + (0.0 if sink is None else np.exp(sink[h] - m))
+            out[b, h] = e @ v / den
+            lse[b, h] = m + np.log(den)
+            ss[b, h] = e.sum() / den
+    return out, lse, ss
+
+
 def _u8arr(x):
     """uint8 codes from a numpy array or a torch tensor of any 1-byte type."""
     if hasattr(x, "detach"):
