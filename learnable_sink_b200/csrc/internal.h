@@ -55,6 +55,8 @@ bool make_tmap_3d_f32(CUtensorMap* map, const void* base, int T, int H, int D, i
                       int box_t);
 bool make_tmap_3d_plain(CUtensorMap* map, const void* base, int T, int H, int D, int box_h,
                         int box_t);
+// uint8 [T, H, D] E4M3 codes, boxes of box_t rows x D bytes (128- or 64-byte swizzle)
+bool make_tmap_codes(CUtensorMap* map, const void* base, int T, int H, int D, int box_t);
 
 // forward
 // fp32 inputs: 3xTF32 tensor-core forward

@@ -3,6 +3,33 @@
 //   x_j = scale <q, k_j>,  l = sum_j e^{x_j - m},  O = sum_j e^{x_j - m} v_j / (l + e^{a - m})
 // over the visible positions j < n, and with a window also j < n_sink or
 // j >= n - window.
+//
+// Bound by HBM (a visible row of K and V is read once and shared by the G query
+// heads of its KV head), as long as the arithmetic stays off the CUDA cores.  So
+// both products run on tcgen05 with the cache as the M side, where its rows lie
+// in shared memory as TMA brought them, whatever their type:
+//   S^T[128 positions x N] = K Q^T     A = K tile, K-major; B = Q, K-major
+//   O^T[D x N]            += V^T P^T   A = V tile, MN-major; B = P, MN-major
+// An instruction costs the same for any N <= 64, so the columns are cheap, and
+// they carry the precision that 8-bit operands lack: a value x is split in
+// rounded terms t0 = r(x), t1 = r((x - t0) c), ..., each in columns of its own and
+// summed, with its factor, in float32.  E4M3 keeps four significant bits: two
+// terms hold a bf16 query exactly (three an f16 one) down to 2^-23 of its row's
+// largest; three terms hold a probability to 2^-12, falling to its last bit at
+// 2^-25 of the largest.  With a 16-bit cache the queries go in as they are and a
+// probability takes two terms (16 bits of it for bf16, 22 for f16).
+//
+// One thread owns one position of a tile: softmax statistics are per thread (l)
+// or voted (the reference maximum moves, for all, when a score passes it by more
+// than 2^2), so a tile needs one barrier among its four warps and no shuffles.  In
+// the 8-bit cache the value scale goes into the probability: e^{x - m} is
+// multiplied by it in the exponent, with a reference of its own.
+//
+// Schedule: the tiles of every (sequence, KV head), in order, are dealt in equal
+// runs to the grid's CTAs; lengths are on the device, so every CTA adds them up
+// for itself.  A run is cut into segments where the pair changes.  A segment that
+// holds all of its pair writes the result; others write (O, m, l) at slot
+// pair + CTA, which no two segments share, and a second kernel joins them.
 #include <cuda_fp8.h>
 
 #include "internal.h"
@@ -12,130 +39,835 @@ namespace sk {
 
 namespace {
 
-constexpr int kTile = 128;  // positions per step
+constexpr int kTile = 128;     // positions per step
+constexpr int kThreads = 224;  // warps 0-3 softmax, 4 TMA, 5 MMA, 6 queries
+constexpr int kMaxCtas = 320;
 
-template <class E>
-__device__ __forceinline__ float cell(const void* pages, long long at, bool fp8) {
-  if (fp8) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(pages)[at], __NV_E4M3);
-    return __half2float(__half(h));
+// ------------------------------------------------------------------ schedule
+// The tiles of a sequence that hold visible positions: [0, ts), then f, f + 1, ...
+struct SeqTiles {
+  int n, ts, f, count;
+  __device__ __forceinline__ int tile(int i) const { return i < ts ? i : f + i - ts; }
+};
+__device__ __forceinline__ SeqTiles seq_tiles(const PagedDecodeProblem& p, int b) {
+  SeqTiles s;
+  const int cap = p.c.max_pages << p.c.page_log2;
+  s.n = min(max(__ldg(p.c.seqlens + b), 0), cap);
+  const int all = s.n / kTile + (s.n % kTile != 0);
+  s.ts = max(all, 1);  // a pair without a key still has a (masked) tile, which writes its result
+  s.f = 0;
+  s.count = s.ts;
+  const int w0 = s.n - p.window;
+  if (p.window > 0 && w0 > p.n_sink) {
+    s.ts = p.n_sink / kTile + (p.n_sink % kTile != 0);
+    s.f = max(w0 / kTile, s.ts);
+    s.count = s.ts + all - s.f;
   }
-  return (float)static_cast<const typename E::T*>(pages)[at];
+  return s;
+}
+__device__ __forceinline__ bool visible(const PagedDecodeProblem& p, int n, int pos) {
+  return pos < n && (p.window <= 0 || pos < p.n_sink || pos >= n - p.window);
 }
 
-// One CTA per (sequence, KV head); thread i scores position i of a tile and sums
-// column i of the values.
-template <class E, int D>
-__global__ void __launch_bounds__(kTile) paged_decode_kernel(PagedDecodeProblem p) {
-  const PagedView& c = p.c;
-  const int b = blockIdx.x / c.Hkv, kvh = blockIdx.x % c.Hkv, G = p.Hq / c.Hkv;
+// A CTA's run of tiles, walked segment by segment (every role walks for itself).
+struct Walk {
+  int b, kvh, t0, cnt;    // the segment: tiles [t0, t0 + cnt) of (b, kvh)
+  SeqTiles seq;
+  long long left;         // tiles of the run from the segment on
+  __device__ __forceinline__ void cut() {
+    cnt = (int)min((long long)(seq.count - t0), left);
+  }
+  __device__ __forceinline__ bool next(const PagedDecodeProblem& p) {
+    left -= cnt;
+    if (left <= 0) return false;
+    t0 = 0;
+    if (++kvh == p.c.Hkv) {
+      kvh = 0;
+      seq = seq_tiles(p, ++b);
+    }
+    cut();
+    return true;
+  }
+};
+struct Start {
+  int b;
+  long long base;  // tiles of one KV head before sequence b
+  long long total, per;
+};
+
+// Adds up the lengths (a slice of the sequences a thread) and finds where this
+// CTA's run begins.
+__device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* st, long long* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  __shared__ float sq[kPagedMaxGroup * D], sp[kPagedMaxGroup * kTile], red[4];
-  __shared__ long long s_row[kTile];
-  __shared__ float s_vs[kTile];
-  const long long cap = (long long)c.max_pages << c.page_log2;
-  int n = max(__ldg(c.seqlens + b), 0);
-  if (n > cap) {
-    if (tid == 0) set_status(c.status, SINKATTN_ERR_BOUNDS);
-    n = (int)cap;
-  }
-  const typename E::T* q = static_cast<const typename E::T*>(p.q) + ((long long)b * p.Hq + kvh * G) * D;
-  for (int i = tid; i < G * D; i += kTile) sq[i] = (float)q[i];
-  float m[kPagedMaxGroup], l[kPagedMaxGroup], acc[kPagedMaxGroup];
+  const int per_thread = (p.c.B + kThreads - 1) / kThreads;
+  const int b0 = tid * per_thread, b1 = min(b0 + per_thread, p.c.B);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) sum += seq_tiles(p, b).count;
+  long long inc = sum;
 #pragma unroll
-  for (int h = 0; h < kPagedMaxGroup; ++h) { m[h] = -INFINITY; l[h] = 0.f; acc[h] = 0.f; }
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
-  for (int j0 = 0; j0 < n; j0 += kTile) {
-    const int j = j0 + tid;
-    bool seen = j < n && (p.window <= 0 || j < p.n_sink || j >= n - p.window);
-    long long row = 0;
-    float ks = 1.f, vs = 1.f;
-    if (seen) {
-      const int page = __ldg(c.table + (long long)b * c.max_pages + (j >> c.page_log2));
-      if (page < 0 || page >= c.n_pages) {
-        set_status(c.status, SINKATTN_ERR_BOUNDS);
-        seen = false;
-      } else {
-        const long long blk = (long long)page * c.Hkv + kvh;
-        row = (blk << c.page_log2) + (j & (c.page_size - 1));
-        if (p.fp8) { ks = c.k_scale[blk]; vs = c.v_scale[blk]; }
-      }
-    }
-    float x[kPagedMaxGroup];
+  long long before = inc - sum, total = 0;
 #pragma unroll
-    for (int h = 0; h < kPagedMaxGroup; ++h) x[h] = 0.f;
-    if (seen)
-      for (int d = 0; d < D; ++d) {
-        const float kv = cell<E>(c.k_pages, row * D + d, p.fp8);
-#pragma unroll
-        for (int h = 0; h < kPagedMaxGroup; ++h)
-          if (h < G) x[h] += sq[h * D + d] * kv;
-      }
-    s_row[tid] = seen ? row : -1;
-    s_vs[tid] = vs;
-#pragma unroll
-    for (int h = 0; h < kPagedMaxGroup; ++h) {
-      if (h >= G) break;
-      x[h] = seen ? x[h] * ks * (p.scale * kLog2e) : -INFINITY;
-      float mx = x[h];
-      for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      __syncthreads();
-      if (lane == 0) red[warp] = mx;
-      __syncthreads();
-      mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-      const float mn = fmaxf(m[h], mx);
-      const float corr = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn);
-      const float pr = x[h] == -INFINITY ? 0.f : exp2f(x[h] - mn);
-      l[h] = l[h] * corr + pr;
-      acc[h] *= corr;
-      m[h] = mn;
-      sp[h * kTile + tid] = pr;
-    }
-    __syncthreads();
-    if (tid < D)
-      for (int i = 0; i < kTile; ++i)
-        if (s_row[i] >= 0) {
-          const float v = cell<E>(c.v_pages, s_row[i] * D + tid, p.fp8) * s_vs[i];
-#pragma unroll
-          for (int h = 0; h < kPagedMaxGroup; ++h)
-            if (h < G) acc[h] += sp[h * kTile + i] * v;
-        }
-    __syncthreads();
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
   }
-#pragma unroll
-  for (int h = 0; h < kPagedMaxGroup; ++h) {
-    if (h >= G) break;
-    float t = l[h];
-    for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    __syncthreads();
-    if (lane == 0) red[warp] = t;
-    __syncthreads();
-    t = (red[0] + red[1]) + (red[2] + red[3]);
-    const float a2 = p.sink ? p.sink[kvh * G + h] * kLog2e : -INFINITY;
-    const float mt = fmaxf(m[h], a2);
-    const float w = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mt);
-    const float den = t * w + (a2 == -INFINITY ? 0.f : exp2f(a2 - mt));
-    const long long row = (long long)b * p.Hq + kvh * G + h;
-    if (tid < D)
-      static_cast<typename E::T*>(p.out)[row * D + tid] =
-          (typename E::T)(den != 0.f ? acc[h] * w / den : 0.f);
-    if (tid == 0) {
-      p.lse[row] = den != 0.f ? (mt + log2f(den)) * kLn2 : -INFINITY;
-      if (p.sink_s) p.sink_s[row] = den != 0.f ? t * w / den : 0.f;
+  total *= p.c.Hkv;
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long x = blockIdx.x * per / p.c.Hkv;  // in tiles of one KV head
+  if (tid == 0) {
+    st->total = total;
+    st->per = per;
+  }
+  if (x >= before && x < before + sum) {
+    int b = b0;
+    for (;;) {
+      const int c = seq_tiles(p, b).count;
+      if (x < before + c) break;
+      before += c;
+      ++b;
     }
+    st->b = b;
+    st->base = before;
   }
 }
 
+// ------------------------------------------------------------------ geometry
+template <class E, int D, bool F8, int GP>
+struct Geo {
+  static constexpr int EB = F8 ? 1 : 2;
+  static constexpr int RB = D * EB;                    // bytes of a row
+  static constexpr int BW = RB < 128 ? RB : 128;       // of a TMA box's row
+  static constexpr int NB = RB / BW;                   // boxes per row
+  static constexpr int TILE = kTile * RB;              // K or V tile
+  static constexpr int QT = F8 ? (E::kFmt == 0 ? 3 : 2) : 1;  // terms of a query
+  static constexpr int PT = F8 ? 3 : 2;                // terms of a probability
+  static constexpr int NQ = (QT * GP + 15) / 16 * 16;  // columns of S^T
+  static constexpr int NP = (PT * GP + 15) / 16 * 16;  // columns of O^T
+  static constexpr int PE = 16 / EB;                   // columns per 16-byte unit of P
+  static constexpr int PBLK = NP / PE;                 // such units per position
+  static constexpr int PBYTES = PBLK * kTile * 16;
+  static constexpr int QBYTES = NQ * RB;
+  static constexpr int KE = 32 / EB;                   // K extent of an instruction
+  static constexpr int TMEM = 2 * NQ + NP <= 128 ? 128 : 256;
+  // A ring of tiles, K and V in turn.  Two CTAs an SM, so that one's segment ends
+  // and waits overlap the other's work; 32 KB tiles leave room for one.
+  static constexpr int CTAS = TILE < 32768 ? 2 : 1;
+  static constexpr int SLOTS = ((CTAS == 2 ? 113664 : 228352) - 2 * QBYTES - 2 * PBYTES - 1024) / TILE;
+  static constexpr int OFF_Q = SLOTS * TILE;
+  static constexpr int OFF_P = OFF_Q + 2 * QBYTES;
+  static constexpr int SMEM = OFF_P + 2 * PBYTES + 1024;  // + room to align the base
+  // factor from one term to the next: the residue of a rounding to EB bytes is
+  // at most 2^-5 (E4M3), 2^-11 (f16) of the value's power of two; bf16 has range
+  // to spare and needs none.  Queries move by 2^4, which keeps every term of a
+  // 448-scaled row in range.
+  static constexpr float TERM = F8 ? 32.f : (E::kFmt == 0 ? 2048.f : 1.f);
+  static_assert(QBYTES % 1024 == 0 && TILE % 1024 == 0, "swizzled tiles start on their pattern");
+  static_assert(SLOTS >= 3, "S of a tile goes ahead of P V of the last one");
+};
+
+// Probabilities are held as 2^kBase e^{x - m}: with a reference that lags by at
+// most 2^kLag they stay within 2^8 (E4M3 reaches 448), as high as they can.
+constexpr float kLag = 2.f, kBase = 6.f;
+
+template <bool F8>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  if constexpr (F8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+  else
+    mma_ss(d, a, b, id, acc);
+}
+// Instruction descriptor: the 16-bit one; kind::f8f6f4 has its fields in the same
+// places (format 0 = E4M3).
+template <class G_, class E, bool F8>
+__host__ __device__ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
+  return idesc_16_f32(F8 ? 0u : E::kFmt, M, N, a_mn, b_mn);
+}
+// Shared-memory descriptor of a K or V tile or a Q block: rows of BW bytes under
+// the swizzle of that width, 8-row groups BW * 8 apart, boxes lbo apart.
+template <int BW>
+__device__ __forceinline__ uint64_t sdesc_rows(uint32_t addr, uint32_t lbo) {
+  const uint64_t type = BW == 128 ? 2 : 4;
+  return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
+         (uint64_t((BW * 8) >> 4) << 32) | (uint64_t(1) << 46) | (type << 61);
+}
+// P: position k's 16-byte unit i at i 2048 + 16 k, no swizzle: 8-position groups
+// 128 bytes apart, units 2048.  A thread stores its position with one vector
+// store a unit, free of bank conflicts.
+__device__ __forceinline__ uint64_t sdesc_p(uint32_t addr) {
+  return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t(128 >> 4) << 16) |
+         (uint64_t((kTile * 16) >> 4) << 32) | (uint64_t(1) << 46);
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 e4m3x2_value(uint32_t two) {
+  const __half2_raw h =
+      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+
+// true on all 128 softmax threads if it is on any
+__device__ __forceinline__ bool any_of_128(bool f) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(uint32_t(f))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+// 2^(a - b), 0 from a = -inf (also over b = -inf)
+__device__ __forceinline__ float ratio2(float a, float b) {
+  return a == -INFINITY ? 0.f : fast_exp2(a - b);
+}
+
+template <int SLOTS>
+struct Bars {
+  uint64_t full[SLOTS], empty[SLOTS];
+  uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], q_free[2], drain;
+};
+
+// workspace: [B Hkv] (first CTA, segments), then the partials
+__host__ __device__ inline size_t meta_floats(long long pairs) {
+  return (size_t)((2 * pairs + 63) / 64 * 64);
+}
+
+// ------------------------------------------------------------------ kernel
+template <class E, int D, bool F8, int GP>
+__global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decode_kernel(
+    const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+    const __grid_constant__ PagedDecodeProblem p) {
+  using G_ = Geo<E, D, F8, GP>;
+  constexpr int SLOTS = G_::SLOTS, NQ = G_::NQ, NP = G_::NP;
+  extern __shared__ uint8_t dsm_raw[];
+  uint8_t* sm =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Bars<SLOTS> bar;
+  __shared__ int abort_s;
+  __shared__ uint32_t tmem_s;
+  __shared__ Start start_s;
+  __shared__ long long warp_s[kThreads / 32];
+  __shared__ float qs_s[4][GP];       // query scales of the last four segments
+  __shared__ float ref_s[2][GP];      // reference maxima of x, and of x + log2(value scale)
+  __shared__ float red_s[4][2][GP];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = p.Hq / p.c.Hkv;
+  const PagedView& c = p.c;
+
+  if (warp == 5) {
+    tmem_alloc(&tmem_s, G_::TMEM);
+    tmem_relinquish();
+  }
+  if (tid == 128) {
+    prefetch_tensormap(&tmap_k);
+    prefetch_tensormap(&tmap_v);
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.pv_done[i], 1);
+      mbar_init(&bar.q_full[i], 1);
+      mbar_init(&bar.q_free[i], 1);
+    }
+    mbar_init(&bar.drain, 1);
+    fence_mbar_init();
+    abort_s = 0;
+  }
+  if (tid < 4 * GP) qs_s[tid / GP][tid % GP] = 0.f;
+  // columns that no head or term owns stay zero
+  for (int i = tid * 16; i < 2 * G_::QBYTES + 2 * G_::PBYTES; i += kThreads * 16)
+    *reinterpret_cast<uint4*>(sm + G_::OFF_Q + i) = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  find_start(p, &start_s, warp_s);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = tmem_s;
+  const uint32_t tm_s = tmem, tm_o = tmem + 2 * NQ;
+
+  const long long per = start_s.per, f0 = (long long)blockIdx.x * per;
+  Walk w;
+  w.left = min(per, start_s.total - f0);
+  const bool work = w.left > 0;
+  if (work) {
+    w.b = start_s.b;
+    w.seq = seq_tiles(p, w.b);
+    const long long rem = f0 - start_s.base * c.Hkv;
+    w.kvh = int(rem / w.seq.count);
+    w.t0 = int(rem % w.seq.count);
+    w.cut();
+  }
+
+  if (!work) {
+    // fewer tiles than CTAs
+  } else if (warp == 4) {
+    // ---------------------------------------------------------------- TMA
+    const int ppt_log2 = 7 - c.page_log2, ppt = 1 << ppt_log2;  // pages per tile
+    int ld = 0;                                                 // tiles (K or V) issued
+    bool ok = true;
+    do {
+      for (int i = 0; i < w.cnt && ok; ++i) {
+        const int page0 = w.seq.tile(w.t0 + i) << ppt_log2;
+        int id = -1;
+        if (lane < ppt) {
+          const int pos = (page0 + lane) << c.page_log2;
+          if (pos < w.seq.n && (p.window <= 0 || pos < p.n_sink ||
+                                pos + c.page_size > w.seq.n - p.window))
+            id = __ldg(c.table + (long long)w.b * c.max_pages + page0 + lane);
+          if (id >= c.n_pages) id = -1;
+        }
+        const uint32_t need = __ballot_sync(0xffffffffu, id >= 0);
+        const uint32_t bytes = __popc(need) * (uint32_t)(c.page_size * G_::RB);
+        const int src = lane / G_::NB, nb = lane % G_::NB;  // this lane's page and box
+        const int my = __shfl_sync(0xffffffffu, id, src);
+        const int row = (my * c.Hkv + w.kvh) << c.page_log2;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++ld) {
+          const int slot = ld % SLOTS;
+          if (ld >= SLOTS) ok = ok && mbar_wait(&bar.empty[slot], (ld / SLOTS - 1) & 1, &abort_s, c.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(&bar.full[slot], bytes);
+          __syncwarp();
+          if (src < ppt && my >= 0)
+            tma_load_3d(sm + slot * G_::TILE + nb * (kTile * G_::BW) +
+                            (src << c.page_log2) * G_::BW,
+                        kv ? &tmap_v : &tmap_k, &bar.full[slot], nb * (G_::BW / G_::EB), 0, row);
+        }
+      }
+    } while (ok && w.next(p));
+    if (!ok)  // leave no copy in flight
+      for (int k = max(ld - SLOTS, 0); k < ld; ++k) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&bar.full[k % SLOTS], (k / SLOTS) & 1))
+          if (clock64() - t0 > kWaitBudgetCycles) break;
+      }
+  } else if (warp == 5) {
+    // ---------------------------------------------------------------- MMA
+    if (lane == 0) {
+      const uint32_t base = smem_u32(sm);
+      bool ok = true;
+      int j = 0, seg = 0;   // tiles, segments begun
+      int pend = -1;        // tile whose P V is not issued yet
+      bool pend_first = false;
+      auto issue_pv = [&]() {
+        const int slot = (2 * pend + 1) % SLOTS;
+        ok = ok && mbar_wait(&bar.p_full[pend & 1], (pend >> 1) & 1, &abort_s, c.status) &&
+             mbar_wait(&bar.full[slot], ((2 * pend + 1) / SLOTS) & 1, &abort_s, c.status);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t ad = sdesc_rows<G_::BW>(base + slot * G_::TILE, kTile * G_::BW);
+        const uint64_t bd = sdesc_p(base + G_::OFF_P + (pend & 1) * G_::PBYTES);
+#pragma unroll
+        for (int k = 0; k < kTile / G_::KE; ++k)
+          mma<F8>(tm_o, sdesc_add(ad, k * G_::KE * G_::BW), sdesc_add(bd, k * G_::KE * 16),
+                  idesc<G_, E, F8>(D, NP, 1, 1), k > 0 || !pend_first);
+        mma_commit(&bar.empty[slot]);
+        mma_commit(&bar.pv_done[pend & 1]);
+        pend = -1;
+      };
+      do {
+        for (int i = 0; i < w.cnt && ok; ++i, ++j) {
+          const int slot = (2 * j) % SLOTS;
+          if (i == 0) ok = ok && mbar_wait(&bar.q_full[seg & 1], (seg >> 1) & 1, &abort_s, c.status);
+          // the next scores ahead of the last tile's values, unless K is late
+          if (pend >= 0 && !mbar_try_wait(&bar.full[slot], ((2 * j) / SLOTS) & 1)) issue_pv();
+          ok = ok && mbar_wait(&bar.full[slot], ((2 * j) / SLOTS) & 1, &abort_s, c.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t ad = sdesc_rows<G_::BW>(base + slot * G_::TILE, 16);
+          const uint64_t bd = sdesc_rows<G_::BW>(base + G_::OFF_Q + (seg & 1) * G_::QBYTES, 16);
+#pragma unroll
+          for (int k = 0; k < G_::RB / 32; ++k) {
+            const int box = k * 32 / G_::BW, in = k * 32 % G_::BW;
+            mma<F8>(tm_s + (j & 1) * NQ, sdesc_add(ad, box * kTile * G_::BW + in),
+                    sdesc_add(bd, box * NQ * G_::BW + in), idesc<G_, E, F8>(kTile, NQ, 0, 0), k > 0);
+          }
+          mma_commit(&bar.empty[slot]);
+          mma_commit(&bar.s_full[j & 1]);
+          if (i == w.cnt - 1) mma_commit(&bar.q_free[seg & 1]);
+          if (pend >= 0) issue_pv();
+          pend = j;
+          pend_first = i == 0;
+        }
+        ++seg;
+      } while (ok && w.next(p));
+      if (ok && pend >= 0) issue_pv();
+      if (!ok) {  // no product may be running when the tensor memory is freed
+        mma_commit(&bar.drain);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&bar.drain, 0))
+          if (clock64() - t0 > kWaitBudgetCycles) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // ---------------------------------------------------------------- queries
+    constexpr int CPL = D / 32;  // columns per lane
+    int seg = 0;
+    bool ok = true;
+    do {
+      if (seg >= 2) ok = mbar_wait(&bar.q_free[seg & 1], ((seg >> 1) - 1) & 1, &abort_s, c.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      uint8_t* qd = sm + G_::OFF_Q + (seg & 1) * G_::QBYTES;
+      const typename E::T* q =
+          static_cast<const typename E::T*>(p.q) + ((long long)w.b * p.Hq + w.kvh * G) * D + lane * CPL;
+      auto at = [&](int r, int byte) {  // row r of the block, swizzled as the tiles are
+        const int box = byte / G_::BW, in = byte % G_::BW, ch = in >> 4;
+        const int x = G_::BW == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
+        return qd + box * (NQ * G_::BW) + r * G_::BW + (x << 4) + (in & 15);
+      };
+      for (int h = 0; h < G; ++h) {
+        uint32_t raw[CPL / 2];
+        if constexpr (CPL == 4) {
+          const uint2 u = __ldg(reinterpret_cast<const uint2*>(q + h * D));
+          raw[0] = u.x;
+          raw[CPL / 2 - 1] = u.y;
+        } else {
+          raw[0] = __ldg(reinterpret_cast<const uint32_t*>(q + h * D));
+        }
+        if constexpr (!F8) {
+#pragma unroll
+          for (int i = 0; i < CPL / 2; ++i)
+            *reinterpret_cast<uint32_t*>(at(h, (lane * CPL + 2 * i) * 2)) = raw[i];
+          if (lane == 0) qs_s[seg & 3][h] = 1.f;
+        } else {
+          float x[CPL];
+          float mx = 0.f;
+          bool odd = false;
+#pragma unroll
+          for (int i = 0; i < CPL / 2; ++i) {
+            const float2 f = E::widen(raw[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+            odd = odd || !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
+          }
+          mx = warp_max(mx);
+          odd = __any_sync(0xffffffffu, odd);
+          // the smallest power of two s with mx <= 448 s (the row's terms reach
+          // 448); an infinity or NaN in the row makes its scores NaN
+          const uint32_t u = __float_as_uint(mx);
+          const int e = max(int(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0), 1);
+          const float inv = odd || mx == 0.f ? 0.f : __uint_as_float(uint32_t(254 - e) << 23);
+          if (lane == 0)
+            qs_s[seg & 3][h] = odd ? __uint_as_float(0x7fffffffu) : __uint_as_float(uint32_t(e) << 23);
+#pragma unroll
+          for (int t = 0; t < G_::QT; ++t) {
+            uint32_t code = 0;
+#pragma unroll
+            for (int i = 0; i < CPL / 2; ++i) {
+              if (t == 0) {
+                x[2 * i] *= inv;
+                x[2 * i + 1] *= inv;
+              }
+              const uint32_t two = e4m3x2(x[2 * i], x[2 * i + 1]);
+              const float2 v = e4m3x2_value(two);
+              x[2 * i] = (x[2 * i] - v.x) * 16.f;
+              x[2 * i + 1] = (x[2 * i + 1] - v.y) * 16.f;
+              code |= two << (16 * i);
+            }
+            uint8_t* dst = at(t * GP + h, lane * CPL);
+            if constexpr (CPL == 4) *reinterpret_cast<uint32_t*>(dst) = code;
+            else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)code;
+          }
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.q_full[seg & 1]);
+      ++seg;
+    } while (w.next(p));
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const uint32_t my_lane = uint32_t(warp * 32) << 16;
+    const float scale_log2 = p.scale * kLog2e;
+    const long long pairs = (long long)c.B * c.Hkv;
+    int2* meta = reinterpret_cast<int2*>(p.part);
+    float* parts = p.part + meta_floats(pairs);
+    int j = 0, seg = 0;
+    // No wait that runs out breaks the loops (each returns at once after the
+    // first): every thread meets every barrier, and the results are undefined.
+    do {
+      float l[GP];
+#pragma unroll
+      for (int h = 0; h < GP; ++h) l[h] = 0.f;
+      if (tid < GP) ref_s[0][tid] = ref_s[1][tid] = -INFINITY;
+      for (int i = 0; i < w.cnt; ++i, ++j) {
+        const int t0 = w.seq.tile(w.t0 + i) * kTile, pos = t0 + tid;
+        bool seen = visible(p, w.seq.n, pos);
+        float ks = scale_log2, lvs = 0.f;
+        if (seen) {
+          const int page = __ldg(c.table + (long long)w.b * c.max_pages + (pos >> c.page_log2));
+          if (page < 0 || page >= c.n_pages) {
+            set_status(c.status, SINKATTN_ERR_BOUNDS);
+            seen = false;
+          } else if constexpr (F8) {
+            const long long blk = (long long)page * c.Hkv + w.kvh;
+            ks *= __ldg(c.k_scale + blk);
+            lvs = log2f(__ldg(c.v_scale + blk));
+          }
+        }
+        mbar_wait(&bar.s_full[j & 1], (j >> 1) & 1, &abort_s, c.status);
+        tc_fence_after();
+        // scores in log2 units; hidden positions at -inf whatever their rows hold
+        float x[GP];
+        {
+          uint32_t r[16];
+#pragma unroll
+          for (int c0 = 0; c0 < NQ; c0 += 16) {
+            tmem_ld16(tm_s + (j & 1) * NQ + c0 + my_lane, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int term = (c0 + k) / GP, h = (c0 + k) % GP;
+              const float v = __uint_as_float(r[k]);
+              if (term == 0) x[h] = v;
+              else if (term < G_::QT) x[h] += v * (term == 1 ? 0.0625f : 0.00390625f);
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          if constexpr (F8) x[h] *= ks * qs_s[seg & 3][h];
+          else x[h] *= ks;
+          x[h] = seen ? x[h] : -INFINITY;
+        }
+        bool moves = i == 0;
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          moves = moves || x[h] > ref_s[0][h] + kLag;
+          if constexpr (F8) moves = moves || x[h] + lvs > ref_s[1][h] + kLag;
+        }
+        if (any_of_128(moves)) {
+          // rare: raise the references to the maxima so far and bring l and O along
+#pragma unroll
+          for (int h = 0; h < GP; ++h) {
+            const float a = warp_max(x[h]);
+            const float b = F8 ? warp_max(x[h] + lvs) : a;
+            if (lane == 0) {
+              red_s[warp][0][h] = a;
+              red_s[warp][1][h] = b;
+            }
+          }
+          named_bar_sync(1, 128);
+          float f[GP];
+#pragma unroll
+          for (int h = 0; h < GP; ++h) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float old = ref_s[k][h];
+              const float now = fmaxf(fmaxf(fmaxf(red_s[0][k][h], red_s[1][k][h]),
+                                            fmaxf(red_s[2][k][h], red_s[3][k][h])), old);
+              const float corr = ratio2(old, now);
+              if (k == 0) l[h] *= corr;
+              f[h] = corr;
+            }
+          }
+          named_bar_sync(1, 128);
+          if (tid < 2 * GP) {
+            const int k = tid / GP, h = tid % GP;
+            ref_s[k][h] = fmaxf(fmaxf(fmaxf(red_s[0][k][h], red_s[1][k][h]),
+                                      fmaxf(red_s[2][k][h], red_s[3][k][h])), ref_s[k][h]);
+          }
+          if (i > 0) {
+            mbar_wait(&bar.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, &abort_s, c.status);
+            tc_fence_after();
+            uint32_t r[16];
+#pragma unroll
+            for (int c0 = 0; c0 < NP; c0 += 16) {
+              tmem_ld16(tm_o + c0 + my_lane, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                r[k] = __float_as_uint(__uint_as_float(r[k]) * f[(c0 + k) % GP]);
+              tmem_st16(tm_o + c0 + my_lane, r);
+            }
+            tmem_st_wait();
+          }
+          named_bar_sync(1, 128);
+        }
+        // P's buffer is free once the values of two tiles ago are done
+        if (j >= 2) mbar_wait(&bar.pv_done[j & 1], ((j >> 1) - 1) & 1, &abort_s, c.status);
+        uint32_t pk[G_::PBLK * 4];
+#pragma unroll
+        for (int k = 0; k < G_::PBLK * 4; ++k) pk[k] = 0u;
+#pragma unroll
+        for (int h = 0; h < GP; h += 2) {
+          float e[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float pr = x[h + k] == -INFINITY ? 0.f : fast_exp2(x[h + k] - ref_s[0][h + k]);
+            l[h + k] += pr;
+            if constexpr (F8) {
+              const float y = x[h + k] + lvs;
+              e[k] = y == -INFINITY ? 0.f : fast_exp2(y - ref_s[1][h + k] + kBase);
+            } else {
+              e[k] = pr * 64.f;
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < G_::PT; ++t) {
+            const int col = t * GP + h;
+            if constexpr (F8) {
+              const uint32_t two = e4m3x2(e[0], e[1]);
+              const float2 v = e4m3x2_value(two);
+              pk[col / 4] |= two << (8 * (col % 4));
+              e[0] = (e[0] - v.x) * G_::TERM;
+              e[1] = (e[1] - v.y) * G_::TERM;
+            } else {
+              const uint32_t two = E::pack(e[0], e[1]);
+              const float2 v = E::widen(two);
+              pk[col / 2] = two;
+              e[0] = (e[0] - v.x) * G_::TERM;
+              e[1] = (e[1] - v.y) * G_::TERM;
+            }
+          }
+        }
+        uint8_t* pd = sm + G_::OFF_P + (j & 1) * G_::PBYTES + tid * 16;
+#pragma unroll
+        for (int k = 0; k < G_::PBLK; ++k)
+          *reinterpret_cast<uint4*>(pd + k * (kTile * 16)) =
+              make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+        if (!seen) {
+          // a hidden row may hold NaN, and 0 NaN is not 0: clear its values
+          const int slot = (2 * j + 1) % SLOTS;
+          mbar_wait(&bar.full[slot], ((2 * j + 1) / SLOTS) & 1, &abort_s, c.status);
+#pragma unroll
+          for (int k = 0; k < G_::RB / 16; ++k)
+            *reinterpret_cast<uint4*>(sm + slot * G_::TILE + (k * 16 / G_::BW) * (kTile * G_::BW) +
+                                      tid * G_::BW + k * 16 % G_::BW) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[j & 1]);
+      }
+      // ------------------------------------------------ the segment's result
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+        if (lane == 0) red_s[warp][0][h] = l[h];
+      }
+      named_bar_sync(1, 128);
+      float acc[GP];
+      mbar_wait(&bar.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, &abort_s, c.status);
+      tc_fence_after();
+      {
+        uint32_t r[16];
+#pragma unroll
+        for (int c0 = 0; c0 < NP; c0 += 16) {
+          tmem_ld16(tm_o + c0 + my_lane, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int term = (c0 + k) / GP, h = (c0 + k) % GP;
+            const float v = __uint_as_float(r[k]);
+            if (term == 0) acc[h] = v;
+            else if (term < G_::PT)
+              acc[h] += v * (term == 1 ? 1.f / G_::TERM : 1.f / (G_::TERM * G_::TERM));
+          }
+        }
+      }
+      const long long pair = (long long)w.b * c.Hkv + w.kvh;
+      const bool final = w.cnt == w.seq.count;
+      // O^T's row of this thread (M = 64: sixteen rows a warp)
+      const int d = D == 128 ? tid : warp * 16 + lane;
+      const bool has_d = D == 128 || lane < 16;
+      float* part = parts + (pair + blockIdx.x) * G * (D + 2);
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        if (h >= G) break;
+        const float m = ref_s[0][h];
+        const float lt = (red_s[0][0][h] + red_s[1][0][h]) + (red_s[2][0][h] + red_s[3][0][h]);
+        // O in units of 2^m
+        const float o = acc[h] * (F8 ? (ref_s[1][h] == -INFINITY
+                                            ? (m == -INFINITY ? 0.f : 1.f)
+                                            : fast_exp2(ref_s[1][h] - m - kBase))
+                                     : 0.015625f);
+        if (final) {
+          const long long row = (long long)w.b * p.Hq + w.kvh * G + h;
+          const float a2 = p.sink ? __ldg(p.sink + w.kvh * G + h) * kLog2e : -INFINITY;
+          const float mt = fmaxf(m, a2), wt = ratio2(m, mt);
+          const float den = lt * wt + ratio2(a2, mt);
+          if (has_d)
+            static_cast<typename E::T*>(p.out)[row * D + d] =
+                (typename E::T)(den != 0.f ? o * wt / den : 0.f);
+          if (tid == h) {
+            p.lse[row] = den != 0.f ? (mt + log2f(den)) * kLn2 : -INFINITY;
+            if (p.sink_s) p.sink_s[row] = den != 0.f ? lt * wt / den : 0.f;
+          }
+        } else {
+          if (has_d) part[h * (D + 2) + d] = o;
+          if (tid == h) {
+            part[h * (D + 2) + D] = m;
+            part[h * (D + 2) + D + 1] = lt;
+          }
+        }
+      }
+      if (w.t0 == 0 && tid == 0) {
+        const long long fp = f0 + (per < start_s.total - f0 ? per : start_s.total - f0) - w.left;
+        if (__ldg(c.seqlens + w.b) > w.seq.n) set_status(c.status, SINKATTN_ERR_BOUNDS);
+        meta[pair] = make_int2(blockIdx.x, int((fp + w.seq.count - 1) / per) - (int)blockIdx.x + 1);
+      }
+      tc_fence_before();
+      named_bar_sync(1, 128);  // the references and sums have been read
+      ++seg;
+    } while (w.next(p));
+  }
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, G_::TMEM);
+  }
+}
+
+// Join a pair's segments and the sink: one CTA per (sequence, query head), a
+// thread a column.  Launched as a programmatic dependent.
+constexpr int kJoinThreads = 128;
+template <class E, int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodeProblem p) {
+  __shared__ float wt_s[kMaxCtas], red_s[2][4];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, G = p.Hq / p.c.Hkv;
+  const long long pair = (long long)b * p.c.Hkv + h / G;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int2 meta = __ldcg(reinterpret_cast<const int2*>(p.part) + pair);
+  const int ns = min(meta.y, kMaxCtas);
+  if (ns <= 1) return;
+  const float* parts = p.part + meta_floats((long long)p.c.B * p.c.Hkv);
+  const long long step = (long long)G * (D + 2);
+  const float* part = parts + (pair + meta.x) * step + (long long)(h % G) * (D + 2);
+  const float a2 = p.sink ? p.sink[h] * kLog2e : -INFINITY;
+  constexpr int R = (kMaxCtas + kJoinThreads - 1) / kJoinThreads;
+  float m[R], l[R], mt = a2;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = r * kJoinThreads + tid;
+    m[r] = i < ns ? __ldcg(part + i * step + D) : -INFINITY;
+    l[r] = i < ns ? __ldcg(part + i * step + D + 1) : 0.f;
+    mt = fmaxf(mt, m[r]);
+  }
+  mt = warp_max(mt);
+  if (lane == 0) red_s[0][warp] = mt;
+  __syncthreads();
+  mt = fmaxf(fmaxf(red_s[0][0], red_s[0][1]), fmaxf(red_s[0][2], red_s[0][3]));
+  float lt = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = r * kJoinThreads + tid;
+    const float wt = ratio2(m[r], mt);
+    if (i < ns) wt_s[i] = wt;
+    lt += l[r] * wt;
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+  if (lane == 0) red_s[1][warp] = lt;
+  __syncthreads();
+  lt = (red_s[1][0] + red_s[1][1]) + (red_s[1][2] + red_s[1][3]);
+  const float den = lt + ratio2(a2, mt);
+  const long long row = (long long)b * p.Hq + h;
+  if (tid < D) {
+    float o = 0.f;
+    for (int i0 = 0; i0 < ns; i0 += 16) {
+      float v[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) v[u] = i0 + u < ns ? __ldcg(part + (i0 + u) * step + tid) : 0.f;
+#pragma unroll
+      for (int u = 0; u < 16; ++u) o += i0 + u < ns ? v[u] * wt_s[i0 + u] : 0.f;
+    }
+    static_cast<typename E::T*>(p.out)[row * D + tid] = (typename E::T)(den != 0.f ? o / den : 0.f);
+  }
+  if (tid == 0) {
+    p.lse[row] = den != 0.f ? (mt + log2f(den)) * kLn2 : -INFINITY;
+    if (p.sink_s) p.sink_s[row] = den != 0.f ? lt / den : 0.f;
+  }
+}
+
+template <class E, int D, bool F8, int GP>
+int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
+  using G_ = Geo<E, D, F8, GP>;
+  const PagedView& c = p.c;
+  const int rows = c.n_pages * c.Hkv * c.page_size;
+  CUtensorMap mk, mv;
+  if (F8 ? !make_tmap_codes(&mk, c.k_pages, rows, 1, D, c.page_size) ||
+               !make_tmap_codes(&mv, c.v_pages, rows, 1, D, c.page_size)
+         : !make_tmap_3d(&mk, c.k_pages, rows, 1, D, 1, c.page_size) ||
+               !make_tmap_3d(&mv, c.v_pages, rows, 1, D, 1, c.page_size))
+    return SINKATTN_ERR_CUDA;
+  auto kern = paged_decode_kernel<E, D, F8, GP>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G_::SMEM) !=
+      cudaSuccess)
+    return SINKATTN_ERR_CUDA;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  // no more CTAs than the tables have tiles
+  const long long tiles = ((long long)c.max_pages * c.page_size + kTile - 1) / kTile;
+  long long grid = tiles * c.B * c.Hkv;
+  if (grid > G_::CTAS * sms) grid = G_::CTAS * sms;
+  if (grid > kMaxCtas) grid = kMaxCtas;
+  record_start(SINKATTN_KERNEL_DECODE, stream);
+  kern<<<(unsigned)grid, kThreads, G_::SMEM, stream>>>(mk, mv, p);
+  record_stop(SINKATTN_KERNEL_DECODE, stream);
+  if (cudaGetLastError() != cudaSuccess) return SINKATTN_ERR_CUDA;
+  if (tiles == 1) return SINKATTN_OK;  // every pair is one segment
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c.B * p.Hq);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<E, D>, p) != cudaSuccess) return SINKATTN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA;
+}
+
+template <class E, int D, bool F8>
+int decode_group(const PagedDecodeProblem& p, cudaStream_t stream) {
+  const int G = p.Hq / p.c.Hkv;
+  if (G <= 4) return decode_cfg<E, D, F8, 4>(p, stream);
+  if (G <= 8) return decode_cfg<E, D, F8, 8>(p, stream);
+  return decode_cfg<E, D, F8, 16>(p, stream);
+}
 template <class E, int D>
 int decode_typed(const PagedDecodeProblem& p, cudaStream_t stream) {
-  paged_decode_kernel<E, D><<<p.c.B * p.c.Hkv, kTile, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA;
+  return p.fp8 ? decode_group<E, D, true>(p, stream) : decode_group<E, D, false>(p, stream);
 }
 
 }  // namespace
 
 size_t paged_decode_part_floats(int B, int Hq, int Hkv, int D, int sms) {
-  return ((size_t)2 * sms + (size_t)B * Hkv) * (Hq / Hkv) * (D + 2);
+  const long long pairs = (long long)B * Hkv;
+  return meta_floats(pairs) + (size_t)(min(2 * sms, kMaxCtas) + pairs) * (Hq / Hkv) * (D + 2);
 }
 
 int launch_paged_decode(const PagedDecodeProblem& p, cudaStream_t s) {
