@@ -25,8 +25,8 @@
 // the 8-bit cache the value scale goes into the probability: e^{x - m} is
 // multiplied by it in the exponent, with a reference of its own.
 //
-// Schedule: the tiles of every (sequence, KV head), in order, are dealt in equal
-// runs to the grid's CTAs; lengths are on the device, so every CTA adds them up
+// Schedule: the tiles of every (sequence, KV head), in order, with a unit for the
+// pair's own cost behind them, are dealt in equal runs to the grid's CTAs; lengths are on the device, so every CTA adds them up
 // for itself.  A run is cut into segments where the pair changes.  A segment that
 // holds all of its pair writes the result; others write (O, m, l) at slot
 // pair + CTA, which no two segments share, and a second kernel joins them.
@@ -40,7 +40,7 @@ namespace sk {
 namespace {
 
 constexpr int kTile = 128;     // positions per step
-constexpr int kThreads = 224;  // warps 0-3 softmax, 4 TMA, 5 MMA, 6 queries
+constexpr int kThreads = 256;  // warps 0-3 softmax, 4 TMA, 5 MMA, 6 queries, 7 page scales
 constexpr int kMaxCtas = 320;
 
 // ------------------------------------------------------------------ schedule
@@ -69,16 +69,25 @@ __device__ __forceinline__ bool visible(const PagedDecodeProblem& p, int n, int 
   return pos < n && (p.window <= 0 || pos < p.n_sink || pos >= n - p.window);
 }
 
-// A CTA's run of tiles, walked segment by segment (every role walks for itself).
+// A pair is worth its tiles and kPairUnits more, for what its ends cost (queries,
+// first references, result) whatever its length.
+constexpr int kPairUnits = 1;
+
+// A CTA's run of units, walked segment by segment (every role walks for itself).
 struct Walk {
-  int b, kvh, t0, cnt;    // the segment: tiles [t0, t0 + cnt) of (b, kvh)
+  int b, kvh, t0, cnt;  // the segment: tiles [t0, t0 + cnt) of (b, kvh)
   SeqTiles seq;
-  long long left;         // tiles of the run from the segment on
+  long long left;       // units of the run from the segment on
   __device__ __forceinline__ void cut() {
     cnt = (int)min((long long)(seq.count - t0), left);
   }
+  // a run that begins behind a pair's tiles begins with the next pair
+  __device__ __forceinline__ bool begin(const PagedDecodeProblem& p) {
+    cut();
+    return left > 0 && (cnt > 0 || next(p));
+  }
   __device__ __forceinline__ bool next(const PagedDecodeProblem& p) {
-    left -= cnt;
+    left -= seq.count + kPairUnits - t0;
     if (left <= 0) return false;
     t0 = 0;
     if (++kvh == p.c.Hkv) {
@@ -91,7 +100,7 @@ struct Walk {
 };
 struct Start {
   int b;
-  long long base;  // tiles of one KV head before sequence b
+  long long base;  // units of one KV head before sequence b
   long long total, per;
 };
 
@@ -102,7 +111,7 @@ __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* s
   const int per_thread = (p.c.B + kThreads - 1) / kThreads;
   const int b0 = tid * per_thread, b1 = min(b0 + per_thread, p.c.B);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += seq_tiles(p, b).count;
+  for (int b = b0; b < b1; ++b) sum += seq_tiles(p, b).count + kPairUnits;
   long long inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -119,7 +128,7 @@ __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* s
   }
   total *= p.c.Hkv;
   const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long x = blockIdx.x * per / p.c.Hkv;  // in tiles of one KV head
+  const long long x = blockIdx.x * per / p.c.Hkv;  // in units of one KV head
   if (tid == 0) {
     st->total = total;
     st->per = per;
@@ -127,7 +136,7 @@ __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* s
   if (x >= before && x < before + sum) {
     int b = b0;
     for (;;) {
-      const int c = seq_tiles(p, b).count;
+      const int c = seq_tiles(p, b).count + kPairUnits;
       if (x < before + c) break;
       before += c;
       ++b;
@@ -231,10 +240,11 @@ __device__ __forceinline__ bool any_of_128(bool f) {
       : "memory");
   return r != 0;
 }
+// the warp's largest x (NaN only if every x is)
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 // 2^(a - b), 0 from a = -inf (also over b = -inf)
 __device__ __forceinline__ float ratio2(float a, float b) {
@@ -267,9 +277,16 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
   __shared__ uint32_t tmem_s;
   __shared__ Start start_s;
   __shared__ long long warp_s[kThreads / 32];
-  __shared__ float qs_s[4][GP];       // query scales of the last four segments
-  __shared__ float ref_s[2][GP];      // reference maxima of x, and of x + log2(value scale)
-  __shared__ float red_s[4][2][GP];
+  __shared__ __align__(16) float qs_s[8][GP];  // query scales of the last eight segments
+  __shared__ float sink_sm[8][GP];             // their sink logits, log2 units
+  // (A segment's entries are read up to its result.  The queries of segment s + 8
+  // are written once the scores of s + 6 are done, which follow the probabilities
+  // of a tile behind segment s + 4.)
+  // reference maxima of x, and of x + log2(value scale), what they were raised by
+  // last (a factor), and each warp's maxima or sums
+  __shared__ __align__(16) float ref_s[2][GP], corr_s[2][GP], red_s[4][2 * GP];
+  // a tile's pages: score factor and log2 of the value scale (NaN: outside the pool)
+  __shared__ float2 page_s[2][8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.Hq / p.c.Hkv;
   const PagedView& c = p.c;
@@ -286,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
       mbar_init(&bar.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.s_full[i], 2);  // scores, and their pages' scales
       mbar_init(&bar.p_full[i], 4);
       mbar_init(&bar.pv_done[i], 1);
       mbar_init(&bar.q_full[i], 1);
@@ -296,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
     fence_mbar_init();
     abort_s = 0;
   }
-  if (tid < 4 * GP) qs_s[tid / GP][tid % GP] = 0.f;
+  if (tid < 8 * GP) qs_s[tid / GP][tid % GP] = 0.f;
   // columns that no head or term owns stay zero
   for (int i = tid * 16; i < 2 * G_::QBYTES + 2 * G_::PBYTES; i += kThreads * 16)
     *reinterpret_cast<uint4*>(sm + G_::OFF_Q + i) = make_uint4(0u, 0u, 0u, 0u);
@@ -311,19 +328,21 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
 
   const long long per = start_s.per, f0 = (long long)blockIdx.x * per;
   Walk w;
-  w.left = min(per, start_s.total - f0);
-  const bool work = w.left > 0;
+  const long long run = min(per, start_s.total - f0);
+  w.left = run;
+  bool work = w.left > 0;
   if (work) {
     w.b = start_s.b;
     w.seq = seq_tiles(p, w.b);
     const long long rem = f0 - start_s.base * c.Hkv;
-    w.kvh = int(rem / w.seq.count);
-    w.t0 = int(rem % w.seq.count);
-    w.cut();
+    const int units = w.seq.count + kPairUnits;
+    w.kvh = int(rem / units);
+    w.t0 = int(rem - (long long)w.kvh * units);
+    work = w.begin(p);
   }
 
   if (!work) {
-    // fewer tiles than CTAs
+    // less work than CTAs
   } else if (warp == 4) {
     // ---------------------------------------------------------------- TMA
     const int ppt_log2 = 7 - c.page_log2, ppt = 1 << ppt_log2;  // pages per tile
@@ -431,10 +450,8 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
     int seg = 0;
     bool ok = true;
     do {
-      if (seg >= 2) ok = mbar_wait(&bar.q_free[seg & 1], ((seg >> 1) - 1) & 1, &abort_s, c.status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       uint8_t* qd = sm + G_::OFF_Q + (seg & 1) * G_::QBYTES;
+      const float a2 = p.sink && lane < G ? __ldg(p.sink + w.kvh * G + lane) * kLog2e : -INFINITY;
       const typename E::T* q =
           static_cast<const typename E::T*>(p.q) + ((long long)w.b * p.Hq + w.kvh * G) * D + lane * CPL;
       auto at = [&](int r, int byte) {  // row r of the block, swizzled as the tiles are
@@ -442,20 +459,31 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
         const int x = G_::BW == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
         return qd + box * (NQ * G_::BW) + r * G_::BW + (x << 4) + (in & 15);
       };
-      for (int h = 0; h < G; ++h) {
-        uint32_t raw[CPL / 2];
+      uint32_t raws[GP][CPL / 2];
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {  // every head's loads in flight at once
+        if (h >= G) continue;
         if constexpr (CPL == 4) {
           const uint2 u = __ldg(reinterpret_cast<const uint2*>(q + h * D));
-          raw[0] = u.x;
-          raw[CPL / 2 - 1] = u.y;
+          raws[h][0] = u.x;
+          raws[h][CPL / 2 - 1] = u.y;
         } else {
-          raw[0] = __ldg(reinterpret_cast<const uint32_t*>(q + h * D));
+          raws[h][0] = __ldg(reinterpret_cast<const uint32_t*>(q + h * D));
         }
+      }
+      if (seg >= 2) ok = mbar_wait(&bar.q_free[seg & 1], ((seg >> 1) - 1) & 1, &abort_s, c.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane < GP) sink_sm[seg & 7][lane] = a2;
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        if (h >= G) continue;
+        const uint32_t(&raw)[CPL / 2] = raws[h];
         if constexpr (!F8) {
 #pragma unroll
           for (int i = 0; i < CPL / 2; ++i)
             *reinterpret_cast<uint32_t*>(at(h, (lane * CPL + 2 * i) * 2)) = raw[i];
-          if (lane == 0) qs_s[seg & 3][h] = 1.f;
+          if (lane == 0) qs_s[seg & 7][h] = 1.f;
         } else {
           float x[CPL];
           float mx = 0.f;
@@ -476,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
           const int e = max(int(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0), 1);
           const float inv = odd || mx == 0.f ? 0.f : __uint_as_float(uint32_t(254 - e) << 23);
           if (lane == 0)
-            qs_s[seg & 3][h] = odd ? __uint_as_float(0x7fffffffu) : __uint_as_float(uint32_t(e) << 23);
+            qs_s[seg & 7][h] = odd ? __uint_as_float(0x7fffffffu) : __uint_as_float(uint32_t(e) << 23);
 #pragma unroll
           for (int t = 0; t < G_::QT; ++t) {
             uint32_t code = 0;
@@ -503,12 +531,60 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
       if (lane == 0) mbar_arrive(&bar.q_full[seg & 1]);
       ++seg;
     } while (w.next(p));
+  } else if (warp == 7) {
+    // ---------------------------------------------------------------- page scales
+    const int ppt_log2 = 7 - c.page_log2, ppt = 1 << ppt_log2;
+    const float scale_log2 = p.scale * kLog2e;
+    int j = 0;
+    bool ok = true;
+    do {
+      auto load_id = [&](int i) {
+        int id = -2;  // no visible position
+        if (lane < ppt && i < w.cnt) {
+          const int page = (w.seq.tile(w.t0 + i) << ppt_log2) + lane;
+          const int pos = page << c.page_log2;
+          if (pos < w.seq.n && (p.window <= 0 || pos < p.n_sink ||
+                                pos + c.page_size > w.seq.n - p.window)) {
+            id = __ldg(c.table + (long long)w.b * c.max_pages + page);
+            if (id < 0 || id >= c.n_pages) {
+              set_status(c.status, SINKATTN_ERR_BOUNDS);
+              id = -1;
+            }
+          }
+        }
+        return id;
+      };
+      int id = load_id(0);
+      if (w.t0 == 0 && lane == 0) {
+        // where the join finds the pair's segments
+        const long long pair = (long long)w.b * c.Hkv + w.kvh;
+        const long long first = f0 + run - w.left;
+        reinterpret_cast<int2*>(p.part)[pair] =
+            make_int2(blockIdx.x, int((first + w.seq.count - 1) / per) - (int)blockIdx.x + 1);
+        if (__ldg(c.seqlens + w.b) > w.seq.n) set_status(c.status, SINKATTN_ERR_BOUNDS);
+      }
+      for (int i = 0; i < w.cnt; ++i, ++j) {
+        float2 v = make_float2(scale_log2, 1.f);
+        if (F8 && id >= 0) {
+          const long long blk = (long long)id * c.Hkv + w.kvh;
+          v.x *= __ldg(c.k_scale + blk);
+          v.y = __ldg(c.v_scale + blk);
+        }
+        const bool outside = id == -1;
+        id = load_id(i + 1);
+        v.y = outside ? __uint_as_float(0x7fffffffu) : F8 ? log2f(v.y) : 0.f;
+        if (j >= 2) ok = mbar_wait(&bar.p_full[j & 1], ((j >> 1) - 1) & 1, &abort_s, c.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane < ppt) page_s[j & 1][lane] = v;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.s_full[j & 1]);
+      }
+    } while (ok && w.next(p));
   } else {
     // ---------------------------------------------------------------- softmax
     const uint32_t my_lane = uint32_t(warp * 32) << 16;
-    const float scale_log2 = p.scale * kLog2e;
     const long long pairs = (long long)c.B * c.Hkv;
-    int2* meta = reinterpret_cast<int2*>(p.part);
     float* parts = p.part + meta_floats(pairs);
     int j = 0, seg = 0;
     // No wait that runs out breaks the loops (each returns at once after the
@@ -520,41 +596,29 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
       if (tid < GP) ref_s[0][tid] = ref_s[1][tid] = -INFINITY;
       for (int i = 0; i < w.cnt; ++i, ++j) {
         const int t0 = w.seq.tile(w.t0 + i) * kTile, pos = t0 + tid;
-        bool seen = visible(p, w.seq.n, pos);
-        float ks = scale_log2, lvs = 0.f;
-        if (seen) {
-          const int page = __ldg(c.table + (long long)w.b * c.max_pages + (pos >> c.page_log2));
-          if (page < 0 || page >= c.n_pages) {
-            set_status(c.status, SINKATTN_ERR_BOUNDS);
-            seen = false;
-          } else if constexpr (F8) {
-            const long long blk = (long long)page * c.Hkv + w.kvh;
-            ks *= __ldg(c.k_scale + blk);
-            lvs = log2f(__ldg(c.v_scale + blk));
-          }
-        }
         mbar_wait(&bar.s_full[j & 1], (j >> 1) & 1, &abort_s, c.status);
         tc_fence_after();
+        const float2 page = page_s[j & 1][tid >> c.page_log2];
+        const bool seen = visible(p, w.seq.n, pos) && !isnan(page.y);
+        const float ks = page.x, lvs = seen ? page.y : 0.f;
         // scores in log2 units; hidden positions at -inf whatever their rows hold
         float x[GP];
         {
-          uint32_t r[16];
+          uint32_t r[NQ / 16][16];
 #pragma unroll
-          for (int c0 = 0; c0 < NQ; c0 += 16) {
-            tmem_ld16(tm_s + (j & 1) * NQ + c0 + my_lane, r);
-            tmem_ld_wait();
+          for (int k = 0; k < NQ / 16; ++k) tmem_ld16(tm_s + (j & 1) * NQ + k * 16 + my_lane, r[k]);
+          tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int term = (c0 + k) / GP, h = (c0 + k) % GP;
-              const float v = __uint_as_float(r[k]);
-              if (term == 0) x[h] = v;
-              else if (term < G_::QT) x[h] += v * (term == 1 ? 0.0625f : 0.00390625f);
-            }
+          for (int k = 0; k < NQ; ++k) {
+            const int term = k / GP, h = k % GP;
+            const float v = __uint_as_float(r[k / 16][k % 16]);
+            if (term == 0) x[h] = v;
+            else if (term < G_::QT) x[h] += v * (term == 1 ? 0.0625f : 0.00390625f);
           }
         }
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
-          if constexpr (F8) x[h] *= ks * qs_s[seg & 3][h];
+          if constexpr (F8) x[h] *= ks * qs_s[seg & 7][h];
           else x[h] *= ks;
           x[h] = seen ? x[h] : -INFINITY;
         }
@@ -565,39 +629,33 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
           if constexpr (F8) moves = moves || x[h] + lvs > ref_s[1][h] + kLag;
         }
         if (any_of_128(moves)) {
-          // rare: raise the references to the maxima so far and bring l and O along
+          // rare: raise the references to the maxima so far, and bring l and O along
+          float mine = 0.f;
 #pragma unroll
           for (int h = 0; h < GP; ++h) {
             const float a = warp_max(x[h]);
-            const float b = F8 ? warp_max(x[h] + lvs) : a;
-            if (lane == 0) {
-              red_s[warp][0][h] = a;
-              red_s[warp][1][h] = b;
+            mine = lane == h ? a : mine;
+            if constexpr (F8) {
+              const float b = warp_max(x[h] + lvs);
+              mine = lane == GP + h ? b : mine;
             }
           }
+          if (lane < (F8 ? 2 : 1) * GP) red_s[warp][lane] = mine;
           named_bar_sync(1, 128);
-          float f[GP];
-#pragma unroll
-          for (int h = 0; h < GP; ++h) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float old = ref_s[k][h];
-              const float now = fmaxf(fmaxf(fmaxf(red_s[0][k][h], red_s[1][k][h]),
-                                            fmaxf(red_s[2][k][h], red_s[3][k][h])), old);
-              const float corr = ratio2(old, now);
-              if (k == 0) l[h] *= corr;
-              f[h] = corr;
-            }
-          }
-          named_bar_sync(1, 128);
-          if (tid < 2 * GP) {
+          if (tid < (F8 ? 2 : 1) * GP) {
             const int k = tid / GP, h = tid % GP;
-            ref_s[k][h] = fmaxf(fmaxf(fmaxf(red_s[0][k][h], red_s[1][k][h]),
-                                      fmaxf(red_s[2][k][h], red_s[3][k][h])), ref_s[k][h]);
+            const float old = ref_s[k][h];
+            const float now = fmaxf(fmaxf(fmaxf(red_s[0][tid], red_s[1][tid]),
+                                          fmaxf(red_s[2][tid], red_s[3][tid])), old);
+            ref_s[k][h] = now;
+            corr_s[k][h] = ratio2(old, now);
           }
+          named_bar_sync(1, 128);
           if (i > 0) {
             mbar_wait(&bar.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, &abort_s, c.status);
             tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < GP; ++h) l[h] *= corr_s[0][h];
             uint32_t r[16];
 #pragma unroll
             for (int c0 = 0; c0 < NP; c0 += 16) {
@@ -605,15 +663,14 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
               tmem_ld_wait();
 #pragma unroll
               for (int k = 0; k < 16; ++k)
-                r[k] = __float_as_uint(__uint_as_float(r[k]) * f[(c0 + k) % GP]);
+                r[k] = __float_as_uint(__uint_as_float(r[k]) * corr_s[F8][(c0 + k) % GP]);
               tmem_st16(tm_o + c0 + my_lane, r);
             }
             tmem_st_wait();
           }
-          named_bar_sync(1, 128);
         }
-        // P's buffer is free once the values of two tiles ago are done
-        if (j >= 2) mbar_wait(&bar.pv_done[j & 1], ((j >> 1) - 1) & 1, &abort_s, c.status);
+        // P's buffer is free: the commit behind these scores covers the products
+        // issued before them, P V of two tiles ago among them
         uint32_t pk[G_::PBLK * 4];
 #pragma unroll
         for (int k = 0; k < G_::PBLK * 4; ++k) pk[k] = 0u;
@@ -673,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
       for (int h = 0; h < GP; ++h) {
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-        if (lane == 0) red_s[warp][0][h] = l[h];
+        if (lane == 0) red_s[warp][h] = l[h];
       }
       named_bar_sync(1, 128);
       float acc[GP];
@@ -705,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
       for (int h = 0; h < GP; ++h) {
         if (h >= G) break;
         const float m = ref_s[0][h];
-        const float lt = (red_s[0][0][h] + red_s[1][0][h]) + (red_s[2][0][h] + red_s[3][0][h]);
+        const float lt = (red_s[0][h] + red_s[1][h]) + (red_s[2][h] + red_s[3][h]);
         // O in units of 2^m
         const float o = acc[h] * (F8 ? (ref_s[1][h] == -INFINITY
                                             ? (m == -INFINITY ? 0.f : 1.f)
@@ -713,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
                                      : 0.015625f);
         if (final) {
           const long long row = (long long)w.b * p.Hq + w.kvh * G + h;
-          const float a2 = p.sink ? __ldg(p.sink + w.kvh * G + h) * kLog2e : -INFINITY;
+          const float a2 = sink_sm[seg & 7][h];
           const float mt = fmaxf(m, a2), wt = ratio2(m, mt);
           const float den = lt * wt + ratio2(a2, mt);
           if (has_d)
@@ -730,11 +787,6 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
             part[h * (D + 2) + D + 1] = lt;
           }
         }
-      }
-      if (w.t0 == 0 && tid == 0) {
-        const long long fp = f0 + (per < start_s.total - f0 ? per : start_s.total - f0) - w.left;
-        if (__ldg(c.seqlens + w.b) > w.seq.n) set_status(c.status, SINKATTN_ERR_BOUNDS);
-        meta[pair] = make_int2(blockIdx.x, int((fp + w.seq.count - 1) / per) - (int)blockIdx.x + 1);
       }
       tc_fence_before();
       named_bar_sync(1, 128);  // the references and sums have been read

@@ -512,7 +512,7 @@ class PagedCache:
     are checked once, here, and kept; their contents may change between calls."""
 
     __slots__ = ("k_pages", "v_pages", "block_table", "cache_seqlens", "k_scale", "v_scale",
-                 "device", "B", "Hkv", "D", "_c", "_ref")
+                 "device", "B", "Hkv", "D", "_c", "_ref", "_dev")
 
     def __init__(self, k_pages, v_pages, block_table, cache_seqlens, k_scale=None, v_scale=None):
         fn = "PagedCache"
@@ -543,6 +543,7 @@ class PagedCache:
         self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
         self.block_table, self.cache_seqlens = block_table, cache_seqlens
         self.device, self.B, self.Hkv, self.D = k_pages.device, B, Hkv, D
+        self._dev = k_pages.get_device()
         self._c = CPagedCache(k_pages.data_ptr(), v_pages.data_ptr(),
                               None if k_scale is None else k_scale.data_ptr(),
                               None if v_scale is None else v_scale.data_ptr(),
@@ -560,73 +561,104 @@ def _one_device(fn, *ts):
 
 def _current(fn, dev):
     """The library launches on the current device."""
-    if dev.index != torch.cuda.current_device():
-        raise SinkAttnError(fn, 1, f"tensors on {dev}, current device "
+    if dev != torch.cuda.current_device():
+        raise SinkAttnError(fn, 1, f"tensors on cuda:{dev}, current device "
                                    f"cuda:{torch.cuda.current_device()}")
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+# torch.cuda.current_stream() builds an object around this handle (3 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _tokens(fn, name, t, shape, dtype, dev):
-    """A packed [T, H, D] input whose tokens may be strided (a view of a fused
-    projection); returns the token stride in elements."""
+def _handle(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev)
+
+
+# The paged calls serve single tokens, where the host's time counts: their checks
+# are plain comparisons, and what was wrong is put in words only once one fails.
+
+
+def _plain(t, shape, dtype, dev):
+    """t (if any) is contiguous, of this shape and type, on device dev."""
+    return t is None or (t.shape == shape and t.dtype == dtype and t.get_device() == dev
+                         and t.is_contiguous())
+
+
+def _refuse_plain(fn, name, t, shape, dtype, dev):
     _shape(fn, name, t, shape, dtype)
-    _want(fn, t.device == dev, f"{name} is on {t.device}, the cache on {dev}")
-    _, H, D = shape
-    st = t.stride()
-    if shape[0] <= 1:
-        st = (H * D, st[1], st[2])
-    _want(fn, st[2] == 1 and (H == 1 or st[1] == D), f"{name}: a token's heads must be contiguous")
-    _want(fn, st[0] >= H * D and st[0] % 8 == 0 and t.data_ptr() % 16 == 0,
-          f"{name}: tokens must be 16-byte aligned and not overlap")
-    return st[0]
+    _contig(t)
+    raise SinkAttnError(fn, 1, f"{name} is on {t.device}, the cache on cuda:{dev}")
+
+
+def _token_stride(fn, name, t, shape, dtype, dev):
+    """Checks a packed [T, H, D] input whose tokens may be strided (a view of a
+    fused projection); returns its token stride in elements."""
+    T, H, D = shape
+    if t.shape != shape or t.dtype != dtype:
+        _shape(fn, name, t, shape, dtype)
+    if t.get_device() != dev:
+        raise SinkAttnError(fn, 1, f"{name} is on {t.device}, the cache on cuda:{dev}")
+    s0, s1, s2 = t.stride()
+    if T <= 1:
+        s0 = H * D
+    if s2 != 1 or (H != 1 and s1 != D):
+        raise SinkAttnError(fn, 1, f"{name}: a token's heads must be contiguous")
+    if s0 < H * D or s0 % 8 or t.data_ptr() % 16:
+        raise SinkAttnError(fn, 1, f"{name}: tokens must be 16-byte aligned and not overlap")
+    return s0
 
 
 def _paged_append(fn, call, coded, k, v, cache, cu_new, rope, interleaved, q, q_out, k_out, stream):
-    _want(fn, k.dim() == 3, "k must be [T, Hkv, D]")
-    dev, D = cache.device, cache.D
-    dt = k.dtype
-    pages = cache.k_pages.dtype
+    if k.dim() != 3:
+        raise SinkAttnError(fn, 1, "k must be [T, Hkv, D]")
+    dev, D, B, dt = cache._dev, cache.D, cache.B, k.dtype
     if coded:
         _want(fn, cache.k_scale is not None, "the cache is not an 8-bit cache")
-    else:
-        _want(fn, pages == dt, f"k is {dt}, the pages {pages}")
+    elif cache.k_pages.dtype != dt:
+        raise SinkAttnError(fn, 1, f"k is {dt}, the pages {cache.k_pages.dtype}")
     T = k.shape[0]
     kv = (T, cache.Hkv, D)
-    ks = _tokens(fn, "k", k, kv, dt, dev)
-    vs = _tokens(fn, "v", v, kv, dt, dev)
-    Hq = qs = 0
+    ks = _token_stride(fn, "k", k, kv, dt, dev)
+    vs = _token_stride(fn, "v", v, kv, dt, dev)
+    Hq = qs = rot = n_pos = 0
     if q is not None:
-        _want(fn, q.dim() == 3, "q must be [T, Hq, D]")
+        if q.dim() != 3:
+            raise SinkAttnError(fn, 1, "q must be [T, Hq, D]")
         Hq = q.shape[1]
-        qs = _tokens(fn, "q", q, (T, Hq, D), dt, dev)
+        qs = _token_stride(fn, "q", q, (T, Hq, D), dt, dev)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
-    _want(fn, q is not None or q_out is None, "q_out without q")
-    for name, t, shape in (("q_out", q_out, (T, Hq, D)), ("k_out", k_out, kv)):
-        if t is not None:
-            _shape(fn, name, t, shape, dt)
-            _want(fn, t.device == dev and t.is_contiguous(),
-                  f"{name} must be contiguous, on the cache's device")
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+        elif not _plain(q_out, (T, Hq, D), dt, dev):
+            _refuse_plain(fn, "q_out", q_out, (T, Hq, D), dt, dev)
+    elif q_out is not None:
+        raise SinkAttnError(fn, 1, "q_out without q")
+    if not _plain(k_out, kv, dt, dev):
+        _refuse_plain(fn, "k_out", k_out, kv, dt, dev)
     if cu_new is None:
-        _want(fn, T == cache.B, f"{T} tokens for {cache.B} sequences without cu_new")
-    else:
-        _shape(fn, "cu_new", cu_new, (cache.B + 1,), torch.int32)
-        _want(fn, cu_new.device == dev and cu_new.is_contiguous(),
-              "cu_new must be contiguous, on the cache's device")
-    rot = n_pos = 0
+        if T != B:
+            raise SinkAttnError(fn, 1, f"{T} tokens for {B} sequences without cu_new")
+    elif not _plain(cu_new, (B + 1,), torch.int32, dev):
+        _refuse_plain(fn, "cu_new", cu_new, (B + 1,), torch.int32, dev)
     if rope is not None:
-        _want(fn, rope.dim() == 2 and rope.dtype == torch.float32 and rope.device == dev
-              and rope.is_contiguous(), "rope must be float32 [n_pos, rot_dim] on the cache's device")
+        if rope.dim() != 2 or not _plain(rope, rope.shape, torch.float32, dev):
+            raise SinkAttnError(fn, 1, "rope must be float32 [n_pos, rot_dim], contiguous, on the "
+                                       "cache's device")
         n_pos, rot = rope.shape
-        _want(fn, n_pos > 0 and rot % 16 == 0 and 16 <= rot <= D,
-              f"rot_dim {rot}: a multiple of 16 up to {D}")
+        if n_pos < 1 or rot % 16 or not 16 <= rot <= D:
+            raise SinkAttnError(fn, 1, f"rot_dim {rot}: a multiple of 16 up to {D}")
     _current(fn, dev)
-    _check(fn, call(_dt(k), T, Hq, cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, _addr(q), qs,
-                    _addr(cu_new), _addr(rope), rot, n_pos, 1 if interleaved else 0, _addr(q_out),
-                    _addr(k_out), _stream(stream)))
+    rc = call(_dt(k), T, Hq, cache._ref, k.data_ptr(), ks, v.data_ptr(), vs,
+              None if q is None else q.data_ptr(), qs,
+              None if cu_new is None else cu_new.data_ptr(),
+              None if rope is None else rope.data_ptr(), rot, n_pos, 1 if interleaved else 0,
+              None if q_out is None else q_out.data_ptr(),
+              None if k_out is None else k_out.data_ptr(), _handle(stream, dev))
+    if rc:
+        raise SinkAttnError(fn, rc)
     return q_out
 
 
@@ -658,35 +690,37 @@ def paged_decode_workspace_bytes(B, Hq, Hkv, D) -> int:
 
 def _paged_decode(fn, call, coded, q, cache, sink, n_sink, window, scale, stream, workspace, out,
                   lse, sink_s):
-    _want(fn, q.dim() == 3, "q must be [B, Hq, D]")
-    B, Hq, D = q.shape
-    dev = cache.device
-    _want(fn, B == cache.B and D == cache.D, f"q {tuple(q.shape)} and the cache disagree on B or D")
+    if q.dim() != 3 or q.shape[0] != cache.B or q.shape[2] != cache.D:
+        raise SinkAttnError(fn, 1, f"q {tuple(q.shape)} and the cache disagree on B or D: "
+                                   f"[{cache.B}, Hq, {cache.D}]")
+    B, Hq, D = shape = q.shape
+    dev, dt = cache._dev, q.dtype
     if coded:
         _want(fn, cache.k_scale is not None, "the cache is not an 8-bit cache")
-    else:
-        _same_type(fn, q, k_pages=cache.k_pages)
+    elif cache.k_pages.dtype != dt:
+        raise SinkAttnError(fn, 1, f"k_pages is {cache.k_pages.dtype}, expected {dt}")
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if lse is None:
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
     if sink_s is None:
-        sink_s = torch.empty(B, Hq, dtype=torch.float32, device=dev)
+        sink_s = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = torch.empty(max(paged_decode_workspace_bytes(B, Hq, cache.Hkv, D), 16),
-                                dtype=torch.uint8, device=dev)
-    _shape(fn, "out", out, q.shape, q.dtype)
-    _shape(fn, "lse", lse, (B, Hq), torch.float32)
-    _shape(fn, "sink_s", sink_s, (B, Hq), torch.float32)
-    _shape(fn, "learnable_sink", sink, (Hq,), torch.float32)
-    _contig(q, sink, out, lse, sink_s, workspace)
-    _one_device(fn, cache.k_pages, q, sink, out, lse, sink_s, workspace)
+                                dtype=torch.uint8, device=q.device)
+    for name, t, want, kind in (("q", q, shape, dt), ("out", out, shape, dt),
+                                ("lse", lse, (B, Hq), torch.float32),
+                                ("sink_s", sink_s, (B, Hq), torch.float32),
+                                ("learnable_sink", sink, (Hq,), torch.float32),
+                                ("workspace", workspace, workspace.shape, workspace.dtype)):
+        if not _plain(t, want, kind, dev):
+            _refuse_plain(fn, name, t, want, kind, dev)
     _current(fn, dev)
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    _check(fn, call(_dt(q), Hq, scale, q.data_ptr(), cache._ref, int(n_sink), int(window),
-                    _addr(sink), out.data_ptr(), lse.data_ptr(), sink_s.data_ptr(),
-                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                    _stream(stream)))
+    rc = call(_dt(q), Hq, D ** -0.5 if scale is None else scale, q.data_ptr(), cache._ref, n_sink,
+              window, None if sink is None else sink.data_ptr(), out.data_ptr(), lse.data_ptr(),
+              sink_s.data_ptr(), workspace.data_ptr(), workspace.nbytes, _handle(stream, dev))
+    if rc:
+        raise SinkAttnError(fn, rc)
     return out, lse, sink_s
 
 
