@@ -53,32 +53,47 @@ __device__ __forceinline__ int page_of(const PagedView& c, int b, int page_idx) 
 }
 
 // The two 8-element column chunks that a thread owns in every row, so that each
-// rotated pair lies in one thread: chunk j of the row's D/16.
+// rotated pair lies in one thread, and neighbouring threads' chunks side by side
+// (16-byte accesses that meet in one 32-byte sector from one thread instead cost
+// a D = 64 append 10 %).  Thread j of the row's D/16.
 struct Chunks {
-  int a, b;       // first columns
-  bool rotated;
+  int a, b;             // first columns
+  bool rot_a, rot_b;    // whether they are rotated
 };
+template <int D>
 __device__ __forceinline__ Chunks row_chunks(int j, int rot, int interleaved) {
   Chunks c;
-  c.rotated = 16 * j < rot;
-  const bool split = c.rotated && !interleaved;
-  c.a = split ? 8 * j : 16 * j;
-  c.b = split ? rot / 2 + 8 * j : 16 * j + 8;
+  if (interleaved) {
+    c.a = 8 * j;
+    c.b = D / 2 + 8 * j;
+    c.rot_a = c.a < rot;
+    c.rot_b = c.b < rot;
+  } else {
+    // the pairs (i, i + rot/2), then the halves of what is not rotated
+    const int nr = rot / 16;
+    c.rot_a = c.rot_b = j < nr;
+    c.a = j < nr ? 8 * j : rot + 8 * (j - nr);
+    c.b = c.a + (j < nr ? rot / 2 : (D - rot) / 2);
+  }
   return c;
 }
 
-// cosines and sines [8 j, 8 j + 8) of a position: either pairing's angles of
-// the thread's sixteen elements
+// cosines and sines of a position for the thread's sixteen elements: eight
+// consecutive angles, or four for each chunk of neighbouring pairs
 struct Angles {
   float c[8], s[8];
 };
 __device__ __forceinline__ void load_angles(Angles& t, const float* rope, long long pos, int rot,
-                                            int j) {
-  const float4* c = reinterpret_cast<const float4*>(rope + pos * rot + 8 * j);
-  const float4* s = reinterpret_cast<const float4*>(rope + pos * rot + rot / 2 + 8 * j);
+                                            const Chunks& ch, int interleaved) {
+  const float* row = rope + pos * rot;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float4 x = __ldg(c + i), y = __ldg(s + i);
+    const int at = interleaved ? (i ? ch.b : ch.a) / 2 : ch.a + 4 * i;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    if (i ? ch.rot_b : ch.rot_a) {
+      x = __ldg(reinterpret_cast<const float4*>(row + at));
+      y = __ldg(reinterpret_cast<const float4*>(row + rot / 2 + at));
+    }
     t.c[4 * i] = x.x; t.c[4 * i + 1] = x.y; t.c[4 * i + 2] = x.z; t.c[4 * i + 3] = x.w;
     t.s[4 * i] = y.x; t.s[4 * i + 1] = y.y; t.s[4 * i + 2] = y.z; t.s[4 * i + 3] = y.w;
   }
@@ -100,17 +115,19 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     E::pack(x[6], x[7]));
 }
 
-__device__ __forceinline__ void rotate16(float (&a)[8], float (&b)[8], const Angles& t,
-                                         int interleaved) {
-  if (interleaved) {
+__device__ __forceinline__ void rotate_pairs(float (&x)[8], const float* c, const float* s) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-      a[2 * i] = a0 * t.c[i] - a1 * t.s[i];
-      a[2 * i + 1] = a1 * t.c[i] + a0 * t.s[i];
-      b[2 * i] = b0 * t.c[4 + i] - b1 * t.s[4 + i];
-      b[2 * i + 1] = b1 * t.c[4 + i] + b0 * t.s[4 + i];
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float x0 = x[2 * i], x1 = x[2 * i + 1];
+    x[2 * i] = x0 * c[i] - x1 * s[i];
+    x[2 * i + 1] = x1 * c[i] + x0 * s[i];
+  }
+}
+__device__ __forceinline__ void rotate16(float (&a)[8], float (&b)[8], const Angles& t,
+                                         const Chunks& ch, int interleaved) {
+  if (interleaved) {
+    if (ch.rot_a) rotate_pairs(a, t.c, t.s);
+    if (ch.rot_b) rotate_pairs(b, t.c + 4, t.s + 4);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -150,12 +167,29 @@ __device__ __forceinline__ Place place_token(const PagedAppendProblem& p, int t,
 // then Hkv keys, then Hkv values (only the queries when kv = false).  Thread
 // (j, g) of the token's D/16 x NG takes chunk pair j of rows g, g + NG, ...;
 // its angles are loaded once for all of them, and four rows are in flight.
-template <class E, int D>
+template <class E, int D, int U>
 __device__ __forceinline__ void token_rows(const PagedAppendProblem& p, int t, int j, int g,
                                            int NG, bool kv, int lane) {
   using T = typename E::T;
   const int Hq = p.q ? p.Hq : 0, Hkv = p.c.Hkv;
   const int rows = kv ? Hq + 2 * Hkv : Hq;
+  const Chunks ch = row_chunks<D>(j, p.rot, p.interleaved);
+  const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
+  const T* k = static_cast<const T*>(p.k) + t * p.k_stride;
+  const T* v = static_cast<const T*>(p.v) + t * p.v_stride;
+  uint4 xa[U], xb[U];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * NG;
+      if (r < rows) {
+        const T* src = r < Hq ? q + r * D : r < Hq + Hkv ? k + (r - Hq) * D : v + (r - Hq - Hkv) * D;
+        xa[u] = *reinterpret_cast<const uint4*>(src + ch.a);
+        xb[u] = *reinterpret_cast<const uint4*>(src + ch.b);
+      }
+    }
+  };
+  load(g);  // under way while the token's place is looked up
   const Place pl = place_token(p, t, lane);
   if (pl.b < 0) return;
   T* kdst = nullptr;
@@ -169,35 +203,21 @@ __device__ __forceinline__ void token_rows(const PagedAppendProblem& p, int t, i
     vdst = static_cast<T*>(p.c.v_pages) + at;
   }
   const long long head_step = (long long)D << p.c.page_log2;
-  const Chunks ch = row_chunks(j, p.rot, p.interleaved);
   Angles an;
-  if (ch.rotated) load_angles(an, p.rope, pl.pos, p.rot, j);
-  const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
-  const T* k = static_cast<const T*>(p.k) + t * p.k_stride;
-  const T* v = static_cast<const T*>(p.v) + t * p.v_stride;
+  if (ch.rot_a) load_angles(an, p.rope, pl.pos, p.rot, ch, p.interleaved);
   T* qo = static_cast<T*>(p.q_out) + (long long)t * p.Hq * D;
   T* ko = p.k_out && kv ? static_cast<T*>(p.k_out) + (long long)t * Hkv * D : nullptr;
-  constexpr int U = 4;
   for (int r0 = g; r0 < rows; r0 += U * NG) {
-    uint4 xa[U], xb[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * NG;
-      if (r < rows) {
-        const T* src = r < Hq ? q + r * D : r < Hq + Hkv ? k + (r - Hq) * D : v + (r - Hq - Hkv) * D;
-        xa[u] = *reinterpret_cast<const uint4*>(src + ch.a);
-        xb[u] = *reinterpret_cast<const uint4*>(src + ch.b);
-      }
-    }
+    if (r0 != g) load(r0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = r0 + u * NG;
       if (r >= rows) break;
-      if (ch.rotated && r < Hq + Hkv) {
+      if (ch.rot_a && r < Hq + Hkv) {
         float a[8], b[8];
         widen8<E>(xa[u], a);
         widen8<E>(xb[u], b);
-        rotate16(a, b, an, p.interleaved);
+        rotate16(a, b, an, ch, p.interleaved);
         xa[u] = pack8<E>(a);
         xb[u] = pack8<E>(b);
       }
@@ -214,16 +234,22 @@ __device__ __forceinline__ void token_rows(const PagedAppendProblem& p, int t, i
 }
 
 constexpr int kAppendThreads = 256;
+// Rows in flight a thread and blocks an SM: more rows hide latency within a
+// thread, but their registers cost the threads that hide it beside them.
+template <int D>
+struct AppendCfg {
+  static constexpr int ROWS = D == 128 ? 2 : 4, BLOCKS = D == 128 ? 4 : 3;
+};
 
 template <class E, int D>
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedAppendProblem p, int NG) {
+__global__ void __launch_bounds__(kAppendThreads, AppendCfg<D>::BLOCKS) paged_append_kernel(PagedAppendProblem p, int NG) {
   constexpr int NC = D / 16;
   const int per_token = NC * NG;  // a multiple of 32: a warp stays in one token
   const long long t =
       (long long)blockIdx.x * (kAppendThreads / per_token) + threadIdx.x / per_token;
   if (t >= p.T) return;
   const int i = threadIdx.x % per_token;
-  token_rows<E, D>(p, (int)t, i % NC, i / NC, NG, true, threadIdx.x & 31);
+  token_rows<E, D, AppendCfg<D>::ROWS>(p, (int)t, i % NC, i / NC, NG, true, threadIdx.x & 31);
 }
 
 // ---------------------------------------------------------------- 8-bit cache
@@ -259,22 +285,23 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float m) {
   return encode4(a.x * m, a.y * m, b.x * m, b.y * m);
 }
 
-// One block of the grid per touched (page, KV head): warps [0, page/16) take its
-// key rows, sixteen each, the other half of the warps its value rows.  The new
+// One block of the grid per touched (page, KV head): warps [0, page/8) take its
+// key rows, eight each, the other half of the warps its value rows.  The new
 // rows are read once and stay in registers between the block's amax and the
-// encoding.  Blocks behind the pages' rotate the queries.
+// encoding (eight rows a warp keep a thread within 64, so the SM stays full).  Blocks behind the pages' rotate the queries.
 //
 // The pages that a sequence touches need no prefix sum: n tokens touch at most
 // n/page + 2 pages (rounded down), so sequence b owns items
 // [cu[b]/page + 2b, cu[b + 1]/page + 2(b + 1)) and the rest of them are idle.
+constexpr int kBlockRows = 8;  // rows a warp of the 8-bit append
 template <class E, int D>
-__global__ void __launch_bounds__(512) paged_append_fp8_kernel(PagedAppendProblem p, int items,
+__global__ void __launch_bounds__(1024) paged_append_fp8_kernel(PagedAppendProblem p, int items,
                                                               unsigned page_blocks, int NG) {
   using T = typename E::T;
   constexpr int NC = D / 16;         // threads per row
   constexpr int RPP = 32 / NC;       // rows per pass of a warp
-  constexpr int PASSES = 16 / RPP;
-  __shared__ float s_max[16];
+  constexpr int PASSES = kBlockRows / RPP;
+  __shared__ float s_max[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x >= page_blocks) {
     const int per_token = NC * NG;
@@ -282,7 +309,7 @@ __global__ void __launch_bounds__(512) paged_append_fp8_kernel(PagedAppendProble
                         threadIdx.x / per_token;
     const int i = threadIdx.x % per_token;
     if (t < p.T && threadIdx.x / per_token < blockDim.x / per_token)
-      token_rows<E, D>(p, (int)t, i % NC, i / NC, NG, false, lane);
+      token_rows<E, D, 2>(p, (int)t, i % NC, i / NC, NG, false, lane);
     return;
   }
   const PagedView& c = p.c;
@@ -323,9 +350,9 @@ __global__ void __launch_bounds__(512) paged_append_fp8_kernel(PagedAppendProble
 
   const int half = blockDim.x >> 6;  // warps of each of K and V
   const bool is_v = warp >= half;
-  const int row_base = (is_v ? warp - half : warp) * 16;
+  const int row_base = (is_v ? warp - half : warp) * kBlockRows;
   const int j = lane % NC, sub = lane / NC;
-  const Chunks ch = is_v ? Chunks{16 * j, 16 * j + 8, false} : row_chunks(j, p.rot, p.interleaved);
+  const Chunks ch = row_chunks<D>(j, is_v ? 0 : p.rot, p.interleaved);
   const T* src = is_v ? static_cast<const T*>(p.v) : static_cast<const T*>(p.k);
   const long long tstride = is_v ? p.v_stride : p.k_stride;
   float xa[PASSES][8], xb[PASSES][8];
@@ -342,10 +369,10 @@ __global__ void __launch_bounds__(512) paged_append_fp8_kernel(PagedAppendProble
     }
     widen8<E>(ua, xa[u]);
     widen8<E>(ub, xb[u]);
-    if (on && ch.rotated) {
+    if (on && ch.rot_a) {
       Angles an;
-      load_angles(an, p.rope, pos0 + r, p.rot, j);
-      rotate16(xa[u], xb[u], an, p.interleaved);
+      load_angles(an, p.rope, pos0 + r, p.rot, ch, p.interleaved);
+      rotate16(xa[u], xb[u], an, ch, p.interleaved);
     }
     if (on && !is_v && p.k_out) {
       T* ko = static_cast<T*>(p.k_out) + (t * c.Hkv + h) * D;
@@ -403,7 +430,7 @@ int append_typed(const PagedAppendProblem& p, cudaStream_t stream) {
 
 template <class E, int D>
 int append_fp8_typed(const PagedAppendProblem& p, cudaStream_t stream) {
-  const int threads = p.c.page_size / 16 * 64;
+  const int threads = p.c.page_size / kBlockRows * 64;
   const long long items = p.cu ? p.T / p.c.page_size + 2LL * p.c.B : p.c.B;
   const long long pages = items * p.c.Hkv;
   const int NG = 128 / D * 8;  // 64 threads a token: every block size holds whole tokens
