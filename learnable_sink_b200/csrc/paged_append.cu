@@ -288,7 +288,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float m) {
 // One block of the grid per touched (page, KV head): warps [0, page/8) take its
 // key rows, eight each, the other half of the warps its value rows.  The new
 // rows are read once and stay in registers between the block's amax and the
-// encoding (eight rows a warp keep a thread within 64, so the SM stays full).  Blocks behind the pages' rotate the queries.
+// X
 //
 // The pages that a sequence touches need no prefix sum: n tokens touch at most
 // n/page + 2 pages (rounded down), so sequence b owns items
@@ -303,9 +303,12 @@ __global__ void __launch_bounds__(1024) paged_append_fp8_kernel(PagedAppendProbl
   constexpr int PASSES = kBlockRows / RPP;
   __shared__ float s_max[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x >= page_blocks) {
+  // page blocks and query blocks alternate, in proportion, so that one kind's
+  // waits lie under the other's traffic
+  const unsigned before = unsigned((unsigned long long)blockIdx.x * page_blocks / gridDim.x);
+  if (unsigned((blockIdx.x + 1ull) * page_blocks / gridDim.x) == before) {
     const int per_token = NC * NG;
-    const long long t = (long long)(blockIdx.x - page_blocks) * (blockDim.x / per_token) +
+    const long long t = (long long)(blockIdx.x - before) * (blockDim.x / per_token) +
                         threadIdx.x / per_token;
     const int i = threadIdx.x % per_token;
     if (t < p.T && threadIdx.x / per_token < blockDim.x / per_token)
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(1024) paged_append_fp8_kernel(PagedAppendProbl
     return;
   }
   const PagedView& c = p.c;
-  const int item = blockIdx.x / c.Hkv, h = blockIdx.x % c.Hkv;
+  const int item = before / c.Hkv, h = before % c.Hkv;
   // the sequence, and the new tokens [t0, t1) that fall in the item's page
   int b, c0, c1;
   if (p.cu) {
@@ -345,8 +348,6 @@ __global__ void __launch_bounds__(1024) paged_append_fp8_kernel(PagedAppendProbl
   const int pos0 = page_idx << c.page_log2;  // position of the page's row 0
   const int r0 = max(start - pos0, 0), r1 = min(end - pos0, c.page_size);
   if (page_idx < max(first, 0) || r0 >= r1) return;
-  const int page = page_of(c, b, page_idx);
-  if (page < 0) return;
 
   const int half = blockDim.x >> 6;  // warps of each of K and V
   const bool is_v = warp >= half;
@@ -355,6 +356,21 @@ __global__ void __launch_bounds__(1024) paged_append_fp8_kernel(PagedAppendProbl
   const Chunks ch = row_chunks<D>(j, is_v ? 0 : p.rot, p.interleaved);
   const T* src = is_v ? static_cast<const T*>(p.v) : static_cast<const T*>(p.k);
   const long long tstride = is_v ? p.v_stride : p.k_stride;
+  uint4 ua[PASSES], ub[PASSES];
+#pragma unroll
+  for (int u = 0; u < PASSES; ++u) {
+    const int r = row_base + u * RPP + sub;
+    const long long t = (long long)c0 + (pos0 + r - start);
+    ua[u] = ub[u] = make_uint4(0, 0, 0, 0);
+    if (r >= r0 && r < r1 && t >= 0 && t < p.T) {
+      ua[u] = *reinterpret_cast<const uint4*>(src + t * tstride + h * D + ch.a);
+      ub[u] = *reinterpret_cast<const uint4*>(src + t * tstride + h * D + ch.b);
+    }
+  }
+  const int page = page_of(c, b, page_idx);  // looked up under the rows' loads
+  if (page < 0) return;
+  float* scale_at = (is_v ? c.v_scale : c.k_scale) + (long long)page * c.Hkv + h;
+  const float s_old = r0 > 0 ? *scale_at : 0.f;
   float xa[PASSES][8], xb[PASSES][8];
   float amax = 0.f;
 #pragma unroll
@@ -362,13 +378,8 @@ __global__ void __launch_bounds__(1024) paged_append_fp8_kernel(PagedAppendProbl
     const int r = row_base + u * RPP + sub;
     const long long t = (long long)c0 + (pos0 + r - start);
     const bool on = r >= r0 && r < r1 && t >= 0 && t < p.T;
-    uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
-    if (on) {
-      ua = *reinterpret_cast<const uint4*>(src + t * tstride + h * D + ch.a);
-      ub = *reinterpret_cast<const uint4*>(src + t * tstride + h * D + ch.b);
-    }
-    widen8<E>(ua, xa[u]);
-    widen8<E>(ub, xb[u]);
+    widen8<E>(ua[u], xa[u]);
+    widen8<E>(ub[u], xb[u]);
     if (on && ch.rot_a) {
       Angles an;
       load_angles(an, p.rope, pos0 + r, p.rot, ch, p.interleaved);
@@ -380,13 +391,19 @@ __global__ void __launch_bounds__(1024) paged_append_fp8_kernel(PagedAppendProbl
       *reinterpret_cast<uint4*>(ko + ch.b) = pack8<E>(xb[u]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(finite_abs(xa[u][i]), finite_abs(xb[u][i])));
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(xa[u][i]), fabsf(xb[u][i])));
+  }
+  if (amax == INFINITY) {  // rare (a NaN has dropped out already): the finite ones alone
+    amax = 0.f;
+#pragma unroll
+    for (int u = 0; u < PASSES; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        amax = fmaxf(amax, fmaxf(finite_abs(xa[u][i]), finite_abs(xb[u][i])));
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (lane == 0) s_max[warp] = amax;
-  float* scale_at = (is_v ? c.v_scale : c.k_scale) + (long long)page * c.Hkv + h;
-  const float s_old = r0 > 0 ? *scale_at : 0.f;
   __syncthreads();
   amax = 0.f;
   for (int w = 0; w < half; ++w) amax = fmaxf(amax, s_max[(is_v ? half : 0) + w]);
