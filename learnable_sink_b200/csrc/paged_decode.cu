@@ -104,6 +104,12 @@ struct Start {
   long long total, per;
 };
 
+// a / b with the 32-bit division where it will do (the 64-bit one is a long
+// subroutine, and every CTA's start waits for it)
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return (a >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // Adds up the lengths (a slice of the sequences a thread) and finds where this
 // CTA's run begins.
 __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* st, long long* s_warp) {
@@ -127,8 +133,8 @@ __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* s
     total += s_warp[w];
   }
   total *= p.c.Hkv;
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long x = blockIdx.x * per / p.c.Hkv;  // in units of one KV head
+  const long long per = quotient(total + gridDim.x - 1, gridDim.x);
+  const long long x = quotient(blockIdx.x * per, p.c.Hkv);  // in units of one KV head
   if (tid == 0) {
     st->total = total;
     st->per = per;
@@ -318,6 +324,9 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
   for (int i = tid * 16; i < 2 * G_::QBYTES + 2 * G_::PBYTES; i += kThreads * 16)
     *reinterpret_cast<uint4*>(sm + G_::OFF_Q + i) = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  // up to here nothing that another kernel writes was read: this kernel is itself
+  // a programmatic dependent, and its start lies under the end of the last one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   find_start(p, &start_s, warp_s);
   tc_fence_before();
   __syncthreads();
@@ -336,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
     w.seq = seq_tiles(p, w.b);
     const long long rem = f0 - start_s.base * c.Hkv;
     const int units = w.seq.count + kPairUnits;
-    w.kvh = int(rem / units);
+    w.kvh = int(quotient(rem, units));
     w.t0 = int(rem - (long long)w.kvh * units);
     work = w.begin(p);
   }
@@ -809,6 +818,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodePro
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, G = p.Hq / p.c.Hkv;
   const long long pair = (long long)b * p.c.Hkv + h / G;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 meta = __ldcg(reinterpret_cast<const int2*>(p.part) + pair);
   const int ns = min(meta.y, kMaxCtas);
@@ -886,19 +896,23 @@ int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
   if (grid > G_::CTAS * sms) grid = G_::CTAS * sms;
   if (grid > kMaxCtas) grid = kMaxCtas;
   record_start(SINKATTN_KERNEL_DECODE, stream);
-  kern<<<(unsigned)grid, kThreads, G_::SMEM, stream>>>(mk, mv, p);
-  record_stop(SINKATTN_KERNEL_DECODE, stream);
-  if (cudaGetLastError() != cudaSuccess) return SINKATTN_ERR_CUDA;
-  if (tiles == 1) return SINKATTN_OK;  // every pair is one segment
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(c.B * p.Hq);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = G_::SMEM;
+  const cudaError_t rc = cudaLaunchKernelEx(&cfg, kern, mk, mv, p);
+  record_stop(SINKATTN_KERNEL_DECODE, stream);
+  if (rc != cudaSuccess) return SINKATTN_ERR_CUDA;
+  if (tiles == 1) return SINKATTN_OK;  // every pair is one segment
+  cfg.gridDim = dim3(c.B * p.Hq);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
   if (cudaLaunchKernelEx(&cfg, paged_join_kernel<E, D>, p) != cudaSuccess) return SINKATTN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA;
 }
