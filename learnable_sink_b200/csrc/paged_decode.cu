@@ -19,10 +19,13 @@
 // 2^-25 of the largest.  With a 16-bit cache the queries go in as they are and a
 // probability takes two terms (16 bits of it for bf16, 22 for f16).
 //
-// One thread owns one position of a tile: softmax statistics are per thread (l)
-// or voted (the reference maximum moves, for all, when a score passes it by more
-// than 2^2), so a tile needs one barrier among its four warps and no shuffles.  In
-// the 8-bit cache the value scale goes into the probability: e^{x - m} is
+// One thread owns one position of a tile and four query heads: softmax statistics
+// are per thread (l) or voted (the reference maximum moves, for all positions, when
+// a score passes it by more than 2^2), so a tile needs one barrier among four warps
+// and no shuffles.  Up to 16 heads take that many warpgroups, each with columns of
+// its own: a tile's time is latency, and four heads fit 80 registers, so the SM
+// holds enough warps to hide it (eight heads a thread: 1.6 times the time a tile).
+// In the 8-bit cache the value scale goes into the probability: e^{x - m} is
 // multiplied by it in the exponent, with a reference of its own.
 //
 // Schedule: the tiles of every (sequence, KV head), in order, with a unit for the
@@ -40,7 +43,7 @@ namespace sk {
 namespace {
 
 constexpr int kTile = 128;     // positions per step
-constexpr int kThreads = 256;  // warps 0-3 softmax, 4 TMA, 5 MMA, 6 queries, 7 page scales
+constexpr int kHeads = 4;      // query heads per softmax warpgroup
 constexpr int kMaxCtas = 320;
 
 // ------------------------------------------------------------------ schedule
@@ -98,23 +101,34 @@ struct Walk {
     return true;
   }
 };
+// a / b, with the 32-bit division where it will do (the 64-bit one is a long
+// subroutine, and every CTA's start waits for it)
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+// CTA i takes units [run_begin(i), run_begin(i + 1)) of the total; with fewer units
+// than CTAs the first ones take one each, so that a pair's CTAs are consecutive.
+__device__ __forceinline__ long long run_begin(long long total, int i) {
+  const int n = (int)min((long long)gridDim.x, total);
+  return quotient(total * min(i, n), n);
+}
+__device__ __forceinline__ int cta_of(long long total, long long unit) {
+  const int n = (int)min((long long)gridDim.x, total);
+  return (int)quotient((unit + 1) * n - 1, total);
+}
+
 struct Start {
   int b;
-  long long base;  // units of one KV head before sequence b
-  long long total, per;
+  long long base;   // units of one KV head before sequence b
+  long long total;  // units of all
 };
-
-// a / b with the 32-bit division where it will do (the 64-bit one is a long
-// subroutine, and every CTA's start waits for it)
-__device__ __forceinline__ long long quotient(long long a, int b) {
-  return (a >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
-}
 
 // Adds up the lengths (a slice of the sequences a thread) and finds where this
 // CTA's run begins.
+template <int THREADS>
 __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* st, long long* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per_thread = (p.c.B + kThreads - 1) / kThreads;
+  const int per_thread = (p.c.B + THREADS - 1) / THREADS;
   const int b0 = tid * per_thread, b1 = min(b0 + per_thread, p.c.B);
   long long sum = 0;
   for (int b = b0; b < b1; ++b) sum += seq_tiles(p, b).count + kPairUnits;
@@ -128,17 +142,13 @@ __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* s
   __syncthreads();
   long long before = inc - sum, total = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += s_warp[w];
     total += s_warp[w];
   }
   total *= p.c.Hkv;
-  const long long per = quotient(total + gridDim.x - 1, gridDim.x);
-  const long long x = quotient(blockIdx.x * per, p.c.Hkv);  // in units of one KV head
-  if (tid == 0) {
-    st->total = total;
-    st->per = per;
-  }
+  const long long x = quotient(run_begin(total, blockIdx.x), p.c.Hkv);  // units of one KV head
+  if (tid == 0) st->total = total;
   if (x >= before && x < before + sum) {
     int b = b0;
     for (;;) {
@@ -153,7 +163,8 @@ __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* s
 }
 
 // ------------------------------------------------------------------ geometry
-template <class E, int D, bool F8, int GP>
+// NWG softmax warpgroups, of four query heads each.
+template <class E, int D, bool F8, int NWG>
 struct Geo {
   static constexpr int EB = F8 ? 1 : 2;
   static constexpr int RB = D * EB;                    // bytes of a row
@@ -162,18 +173,22 @@ struct Geo {
   static constexpr int TILE = kTile * RB;              // K or V tile
   static constexpr int QT = F8 ? (E::kFmt == 0 ? 3 : 2) : 1;  // terms of a query
   static constexpr int PT = F8 ? 3 : 2;                // terms of a probability
-  static constexpr int NQ = (QT * GP + 15) / 16 * 16;  // columns of S^T
-  static constexpr int NP = (PT * GP + 15) / 16 * 16;  // columns of O^T
-  static constexpr int PE = 16 / EB;                   // columns per 16-byte unit of P
-  static constexpr int PBLK = NP / PE;                 // such units per position
+  // A warpgroup's columns: term t of head h at 4 t + h of 16 bytes' worth, so that
+  // a thread's probabilities are one 16-byte store.
+  static constexpr int COLS = 16 / EB;
+  static constexpr int N = COLS * NWG < 16 ? 16 : COLS * NWG;  // columns of S^T and O^T
+  static constexpr int PBLK = N / COLS;                // 16-byte units per position
   static constexpr int PBYTES = PBLK * kTile * 16;
-  static constexpr int QBYTES = NQ * RB;
+  static constexpr int QBYTES = N * RB;
   static constexpr int KE = 32 / EB;                   // K extent of an instruction
-  static constexpr int TMEM = 2 * NQ + NP <= 128 ? 128 : 256;
-  // A ring of tiles, K and V in turn.  Two CTAs an SM, so that one's segment ends
-  // and waits overlap the other's work; 32 KB tiles leave room for one.
-  static constexpr int CTAS = TILE < 32768 ? 2 : 1;
-  static constexpr int SLOTS = ((CTAS == 2 ? 113664 : 228352) - 2 * QBYTES - 2 * PBYTES - 1024) / TILE;
+  static constexpr int TMEM = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 256;
+  static constexpr int WARPS = 4 * NWG + 4, THREADS = WARPS * 32;
+  // CTAs an SM: one's segment ends and waits overlap the other's work.  32 KB tiles
+  // (or sixteen heads) leave room for one.
+  static constexpr int CTAS = TILE < 32768 && NWG < 4 ? 2 : 1;
+  // A ring of tiles, K and V in turn.
+  static constexpr int SLOTS =
+      ((CTAS == 2 ? 112640 : 227328) - 2 * QBYTES - 2 * PBYTES - 1024) / TILE;
   static constexpr int OFF_Q = SLOTS * TILE;
   static constexpr int OFF_P = OFF_Q + 2 * QBYTES;
   static constexpr int SMEM = OFF_P + 2 * PBYTES + 1024;  // + room to align the base
@@ -182,6 +197,7 @@ struct Geo {
   // to spare and needs none.  Queries move by 2^4, which keeps every term of a
   // 448-scaled row in range.
   static constexpr float TERM = F8 ? 32.f : (E::kFmt == 0 ? 2048.f : 1.f);
+  static_assert((PT > QT ? PT : QT) * kHeads <= COLS, "a warpgroup's columns");
   static_assert(QBYTES % 1024 == 0 && TILE % 1024 == 0, "swizzled tiles start on their pattern");
   static_assert(SLOTS >= 3, "S of a tile goes ahead of P V of the last one");
 };
@@ -204,7 +220,7 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 }
 // Instruction descriptor: the 16-bit one; kind::f8f6f4 has its fields in the same
 // places (format 0 = E4M3).
-template <class G_, class E, bool F8>
+template <class E, bool F8>
 __host__ __device__ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
   return idesc_16_f32(F8 ? 0u : E::kFmt, M, N, a_mn, b_mn);
 }
@@ -233,18 +249,37 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t two) {
   return __half22float2(__half2(h));
 }
 
-// true on all 128 softmax threads if it is on any
-__device__ __forceinline__ bool any_of_128(bool f) {
+// true on all 128 threads of the warpgroup (barrier 1 + wg) if it is on any
+__device__ __forceinline__ bool any_of_128(bool f, int wg) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}\n"
       : "=r"(r)
-      : "r"(uint32_t(f))
+      : "r"(uint32_t(f)), "r"(wg + 1)
       : "memory");
   return r != 0;
+}
+// Lane's row, N consecutive columns (4, 8 or 16).
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
+  if constexpr (N == 16) tmem_ld16(addr, r);
+  else if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+  else
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[N]) {
+  if constexpr (N == 16) tmem_st16(addr, r);
+  else tmem_st8(addr, r);
 }
 // the warp's largest x (NaN only if every x is)
 __device__ __forceinline__ float warp_max(float x) {
@@ -269,12 +304,14 @@ __host__ __device__ inline size_t meta_floats(long long pairs) {
 }
 
 // ------------------------------------------------------------------ kernel
-template <class E, int D, bool F8, int GP>
-__global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decode_kernel(
-    const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-    const __grid_constant__ PagedDecodeProblem p) {
-  using G_ = Geo<E, D, F8, GP>;
-  constexpr int SLOTS = G_::SLOTS, NQ = G_::NQ, NP = G_::NP;
+template <class E, int D, bool F8, int NWG>
+__global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG>::CTAS)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                        const __grid_constant__ CUtensorMap tmap_v,
+                        const __grid_constant__ PagedDecodeProblem p) {
+  using G_ = Geo<E, D, F8, NWG>;
+  constexpr int SLOTS = G_::SLOTS, N = G_::N, COLS = G_::COLS, GP = NWG * kHeads, H = kHeads;
+  constexpr int W_TMA = 4 * NWG, W_MMA = W_TMA + 1, W_Q = W_TMA + 2;
   extern __shared__ uint8_t dsm_raw[];
   uint8_t* sm =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
@@ -282,26 +319,27 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
   __shared__ int abort_s;
   __shared__ uint32_t tmem_s;
   __shared__ Start start_s;
-  __shared__ long long warp_s[kThreads / 32];
+  __shared__ long long warp_s[G_::WARPS];
   __shared__ __align__(16) float qs_s[8][GP];  // query scales of the last eight segments
   __shared__ float sink_sm[8][GP];             // their sink logits, log2 units
   // (A segment's entries are read up to its result.  The queries of segment s + 8
   // are written once the scores of s + 6 are done, which follow the probabilities
   // of a tile behind segment s + 4.)
-  // reference maxima of x, and of x + log2(value scale), what they were raised by
-  // last (a factor), and each warp's maxima or sums
-  __shared__ __align__(16) float ref_s[2][GP], corr_s[2][GP], red_s[4][2 * GP];
+  // For each warpgroup: reference maxima of x and of x + log2(value scale), what they
+  // were raised by last (a factor), each warp's maxima or sums, and the factors of
+  // the result.
+  __shared__ __align__(16) float ref_s[NWG][2][H], corr_s[NWG][2][H], red_s[NWG][4][2 * H], fac_s[NWG][H];
   // a tile's pages: score factor and log2 of the value scale (NaN: outside the pool)
   __shared__ float2 page_s[2][8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.Hq / p.c.Hkv;
   const PagedView& c = p.c;
 
-  if (warp == 5) {
+  if (warp == W_MMA) {
     tmem_alloc(&tmem_s, G_::TMEM);
     tmem_relinquish();
   }
-  if (tid == 128) {
+  if (tid == W_TMA * 32) {
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
     for (int i = 0; i < SLOTS; ++i) {
@@ -310,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 2);  // scores, and their pages' scales
-      mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.p_full[i], 4 * NWG);
       mbar_init(&bar.pv_done[i], 1);
       mbar_init(&bar.q_full[i], 1);
       mbar_init(&bar.q_free[i], 1);
@@ -321,23 +359,23 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
   }
   if (tid < 8 * GP) qs_s[tid / GP][tid % GP] = 0.f;
   // columns that no head or term owns stay zero
-  for (int i = tid * 16; i < 2 * G_::QBYTES + 2 * G_::PBYTES; i += kThreads * 16)
+  for (int i = tid * 16; i < 2 * G_::QBYTES + 2 * G_::PBYTES; i += G_::THREADS * 16)
     *reinterpret_cast<uint4*>(sm + G_::OFF_Q + i) = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   // up to here nothing that another kernel writes was read: this kernel is itself
   // a programmatic dependent, and its start lies under the end of the last one
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  find_start(p, &start_s, warp_s);
+  find_start<G_::THREADS>(p, &start_s, warp_s);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = tmem_s;
-  const uint32_t tm_s = tmem, tm_o = tmem + 2 * NQ;
+  const uint32_t tm_s = tmem, tm_o = tmem + 2 * N;
 
-  const long long per = start_s.per, f0 = (long long)blockIdx.x * per;
+  const long long total = start_s.total;
+  const long long f0 = run_begin(total, blockIdx.x), run = run_begin(total, blockIdx.x + 1) - f0;
   Walk w;
-  const long long run = min(per, start_s.total - f0);
   w.left = run;
   bool work = w.left > 0;
   if (work) {
@@ -352,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
 
   if (!work) {
     // less work than CTAs
-  } else if (warp == 4) {
+  } else if (warp == W_TMA) {
     // ---------------------------------------------------------------- TMA
     const int ppt_log2 = 7 - c.page_log2, ppt = 1 << ppt_log2;  // pages per tile
     int ld = 0;                                                 // tiles (K or V) issued
@@ -394,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
         while (!mbar_try_wait(&bar.full[k % SLOTS], (k / SLOTS) & 1))
           if (clock64() - t0 > kWaitBudgetCycles) break;
       }
-  } else if (warp == 5) {
+  } else if (warp == W_MMA) {
     // ---------------------------------------------------------------- MMA
     if (lane == 0) {
       const uint32_t base = smem_u32(sm);
@@ -413,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
 #pragma unroll
         for (int k = 0; k < kTile / G_::KE; ++k)
           mma<F8>(tm_o, sdesc_add(ad, k * G_::KE * G_::BW), sdesc_add(bd, k * G_::KE * 16),
-                  idesc<G_, E, F8>(D, NP, 1, 1), k > 0 || !pend_first);
+                  idesc<E, F8>(D, N, 1, 1), k > 0 || !pend_first);
         mma_commit(&bar.empty[slot]);
         mma_commit(&bar.pv_done[pend & 1]);
         pend = -1;
@@ -432,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
 #pragma unroll
           for (int k = 0; k < G_::RB / 32; ++k) {
             const int box = k * 32 / G_::BW, in = k * 32 % G_::BW;
-            mma<F8>(tm_s + (j & 1) * NQ, sdesc_add(ad, box * kTile * G_::BW + in),
-                    sdesc_add(bd, box * NQ * G_::BW + in), idesc<G_, E, F8>(kTile, NQ, 0, 0), k > 0);
+            mma<F8>(tm_s + (j & 1) * N, sdesc_add(ad, box * kTile * G_::BW + in),
+                    sdesc_add(bd, box * N * G_::BW + in), idesc<E, F8>(kTile, N, 0, 0), k > 0);
           }
           mma_commit(&bar.empty[slot]);
           mma_commit(&bar.s_full[j & 1]);
@@ -453,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
       }
     }
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == W_Q) {
     // ---------------------------------------------------------------- queries
     constexpr int CPL = D / 32;  // columns per lane
     int seg = 0;
@@ -466,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
       auto at = [&](int r, int byte) {  // row r of the block, swizzled as the tiles are
         const int box = byte / G_::BW, in = byte % G_::BW, ch = in >> 4;
         const int x = G_::BW == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
-        return qd + box * (NQ * G_::BW) + r * G_::BW + (x << 4) + (in & 15);
+        return qd + box * (N * G_::BW) + r * G_::BW + (x << 4) + (in & 15);
       };
       uint32_t raws[GP][CPL / 2];
 #pragma unroll
@@ -491,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
         if constexpr (!F8) {
 #pragma unroll
           for (int i = 0; i < CPL / 2; ++i)
-            *reinterpret_cast<uint32_t*>(at(h, (lane * CPL + 2 * i) * 2)) = raw[i];
+            *reinterpret_cast<uint32_t*>(at(h / H * COLS + h % H, (lane * CPL + 2 * i) * 2)) = raw[i];
           if (lane == 0) qs_s[seg & 7][h] = 1.f;
         } else {
           float x[CPL];
@@ -529,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
               x[2 * i + 1] = (x[2 * i + 1] - v.y) * 16.f;
               code |= two << (16 * i);
             }
-            uint8_t* dst = at(t * GP + h, lane * CPL);
+            uint8_t* dst = at(h / H * COLS + t * H + h % H, lane * CPL);
             if constexpr (CPL == 4) *reinterpret_cast<uint32_t*>(dst) = code;
             else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)code;
           }
@@ -540,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
       if (lane == 0) mbar_arrive(&bar.q_full[seg & 1]);
       ++seg;
     } while (w.next(p));
-  } else if (warp == 7) {
+  } else if (warp == W_Q + 1) {
     // ---------------------------------------------------------------- page scales
     const int ppt_log2 = 7 - c.page_log2, ppt = 1 << ppt_log2;
     const float scale_log2 = p.scale * kLog2e;
@@ -568,8 +606,8 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
         // where the join finds the pair's segments
         const long long pair = (long long)w.b * c.Hkv + w.kvh;
         const long long first = f0 + run - w.left;
-        reinterpret_cast<int2*>(p.part)[pair] =
-            make_int2(blockIdx.x, int((first + w.seq.count - 1) / per) - (int)blockIdx.x + 1);
+        reinterpret_cast<int2*>(p.part)[pair] = make_int2(
+            blockIdx.x, cta_of(total, first + w.seq.count - 1) - (int)blockIdx.x + 1);
         if (__ldg(c.seqlens + w.b) > w.seq.n) set_status(c.status, SINKATTN_ERR_BOUNDS);
       }
       for (int i = 0; i < w.cnt; ++i, ++j) {
@@ -592,142 +630,138 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
     } while (ok && w.next(p));
   } else {
     // ---------------------------------------------------------------- softmax
-    const uint32_t my_lane = uint32_t(warp * 32) << 16;
+    const int wg = NWG == 1 ? 0 : warp >> 2, wt = tid & 127, ww = warp & 3;
+    const int h0 = wg * H;                                    // its first query head
+    const uint32_t my_lane = uint32_t(ww * 32) << 16;
+    const uint32_t my_s = tm_s + wg * COLS + my_lane, my_o = tm_o + wg * COLS + my_lane;
+    float(&ref)[2][H] = ref_s[wg];
+    float(&corr)[2][H] = corr_s[wg];
+    float(&red)[4][2 * H] = red_s[wg];
     const long long pairs = (long long)c.B * c.Hkv;
     float* parts = p.part + meta_floats(pairs);
     int j = 0, seg = 0;
     // No wait that runs out breaks the loops (each returns at once after the
     // first): every thread meets every barrier, and the results are undefined.
     do {
-      float l[GP];
+      float l[H];
 #pragma unroll
-      for (int h = 0; h < GP; ++h) l[h] = 0.f;
-      if (tid < GP) ref_s[0][tid] = ref_s[1][tid] = -INFINITY;
+      for (int h = 0; h < H; ++h) l[h] = 0.f;
+      if (wt < 2 * H) ref[wt / H][wt % H] = -INFINITY;
       for (int i = 0; i < w.cnt; ++i, ++j) {
-        const int t0 = w.seq.tile(w.t0 + i) * kTile, pos = t0 + tid;
+        const int pos = w.seq.tile(w.t0 + i) * kTile + wt;
         mbar_wait(&bar.s_full[j & 1], (j >> 1) & 1, &abort_s, c.status);
         tc_fence_after();
-        const float2 page = page_s[j & 1][tid >> c.page_log2];
+        const float2 page = page_s[j & 1][wt >> c.page_log2];
         const bool seen = visible(p, w.seq.n, pos) && !isnan(page.y);
-        const float ks = page.x, lvs = seen ? page.y : 0.f;
+        const float lvs = seen ? page.y : 0.f;
         // scores in log2 units; hidden positions at -inf whatever their rows hold
-        float x[GP];
-        {
-          uint32_t r[NQ / 16][16];
-#pragma unroll
-          for (int k = 0; k < NQ / 16; ++k) tmem_ld16(tm_s + (j & 1) * NQ + k * 16 + my_lane, r[k]);
+        float x[H];
+        if constexpr (F8) {
+          uint32_t r[16];
+          tmem_ld(my_s + (j & 1) * N, r);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < NQ; ++k) {
-            const int term = k / GP, h = k % GP;
-            const float v = __uint_as_float(r[k / 16][k % 16]);
-            if (term == 0) x[h] = v;
-            else if (term < G_::QT) x[h] += v * (term == 1 ? 0.0625f : 0.00390625f);
+          for (int h = 0; h < H; ++h) {
+            x[h] = __uint_as_float(r[h]) + __uint_as_float(r[H + h]) * 0.0625f;
+            if constexpr (G_::QT == 3) x[h] += __uint_as_float(r[2 * H + h]) * 0.00390625f;
+            x[h] *= page.x * qs_s[seg & 7][h0 + h];
           }
-        }
+        } else {
+          uint32_t r[4];
+          tmem_ld(my_s + (j & 1) * N, r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < GP; ++h) {
-          if constexpr (F8) x[h] *= ks * qs_s[seg & 7][h];
-          else x[h] *= ks;
-          x[h] = seen ? x[h] : -INFINITY;
+          for (int h = 0; h < H; ++h) x[h] = __uint_as_float(r[h]) * page.x;
         }
         bool moves = i == 0;
 #pragma unroll
-        for (int h = 0; h < GP; ++h) {
-          moves = moves || x[h] > ref_s[0][h] + kLag;
-          if constexpr (F8) moves = moves || x[h] + lvs > ref_s[1][h] + kLag;
+        for (int h = 0; h < H; ++h) {
+          x[h] = seen ? x[h] : -INFINITY;
+          moves = moves || x[h] > ref[0][h] + kLag;
+          if constexpr (F8) moves = moves || x[h] + lvs > ref[1][h] + kLag;
         }
-        if (any_of_128(moves)) {
+        if (any_of_128(moves, wg)) {
           // rare: raise the references to the maxima so far, and bring l and O along
           float mine = 0.f;
 #pragma unroll
-          for (int h = 0; h < GP; ++h) {
+          for (int h = 0; h < H; ++h) {
             const float a = warp_max(x[h]);
             mine = lane == h ? a : mine;
             if constexpr (F8) {
               const float b = warp_max(x[h] + lvs);
-              mine = lane == GP + h ? b : mine;
+              mine = lane == H + h ? b : mine;
             }
           }
-          if (lane < (F8 ? 2 : 1) * GP) red_s[warp][lane] = mine;
-          named_bar_sync(1, 128);
-          if (tid < (F8 ? 2 : 1) * GP) {
-            const int k = tid / GP, h = tid % GP;
-            const float old = ref_s[k][h];
-            const float now = fmaxf(fmaxf(fmaxf(red_s[0][tid], red_s[1][tid]),
-                                          fmaxf(red_s[2][tid], red_s[3][tid])), old);
-            ref_s[k][h] = now;
-            corr_s[k][h] = ratio2(old, now);
+          if (lane < (F8 ? 2 : 1) * H) red[ww][lane] = mine;
+          named_bar_sync(1 + wg, 128);
+          if (wt < (F8 ? 2 : 1) * H) {
+            const int k = wt / H, h = wt % H;
+            const float old = ref[k][h];
+            const float now =
+                fmaxf(fmaxf(fmaxf(red[0][wt], red[1][wt]), fmaxf(red[2][wt], red[3][wt])), old);
+            ref[k][h] = now;
+            corr[k][h] = ratio2(old, now);
           }
-          named_bar_sync(1, 128);
+          named_bar_sync(1 + wg, 128);
           if (i > 0) {
             mbar_wait(&bar.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, &abort_s, c.status);
             tc_fence_after();
+            uint32_t r[COLS];
+            tmem_ld(my_o, r);
+            tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < GP; ++h) l[h] *= corr_s[0][h];
-            uint32_t r[16];
+            for (int h = 0; h < H; ++h) l[h] *= corr[0][h];
 #pragma unroll
-            for (int c0 = 0; c0 < NP; c0 += 16) {
-              tmem_ld16(tm_o + c0 + my_lane, r);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                r[k] = __float_as_uint(__uint_as_float(r[k]) * corr_s[F8][(c0 + k) % GP]);
-              tmem_st16(tm_o + c0 + my_lane, r);
-            }
+            for (int k = 0; k < COLS; ++k)
+              r[k] = __float_as_uint(__uint_as_float(r[k]) * corr[F8][k % H]);
+            tmem_st(my_o, r);
             tmem_st_wait();
           }
         }
         // P's buffer is free: the commit behind these scores covers the products
         // issued before them, P V of two tiles ago among them
-        uint32_t pk[G_::PBLK * 4];
+        uint32_t pk[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int k = 0; k < G_::PBLK * 4; ++k) pk[k] = 0u;
-#pragma unroll
-        for (int h = 0; h < GP; h += 2) {
+        for (int h = 0; h < H; h += 2) {
           float e[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float pr = x[h + k] == -INFINITY ? 0.f : fast_exp2(x[h + k] - ref_s[0][h + k]);
+            const float pr = x[h + k] == -INFINITY ? 0.f : fast_exp2(x[h + k] - ref[0][h + k]);
             l[h + k] += pr;
             if constexpr (F8) {
               const float y = x[h + k] + lvs;
-              e[k] = y == -INFINITY ? 0.f : fast_exp2(y - ref_s[1][h + k] + kBase);
+              e[k] = y == -INFINITY ? 0.f : fast_exp2(y - ref[1][h + k] + kBase);
             } else {
               e[k] = pr * 64.f;
             }
           }
 #pragma unroll
           for (int t = 0; t < G_::PT; ++t) {
-            const int col = t * GP + h;
             if constexpr (F8) {
               const uint32_t two = e4m3x2(e[0], e[1]);
               const float2 v = e4m3x2_value(two);
-              pk[col / 4] |= two << (8 * (col % 4));
+              pk[t] |= two << (8 * h);
               e[0] = (e[0] - v.x) * G_::TERM;
               e[1] = (e[1] - v.y) * G_::TERM;
             } else {
               const uint32_t two = E::pack(e[0], e[1]);
               const float2 v = E::widen(two);
-              pk[col / 2] = two;
+              pk[2 * t + h / 2] = two;
               e[0] = (e[0] - v.x) * G_::TERM;
               e[1] = (e[1] - v.y) * G_::TERM;
             }
           }
         }
-        uint8_t* pd = sm + G_::OFF_P + (j & 1) * G_::PBYTES + tid * 16;
-#pragma unroll
-        for (int k = 0; k < G_::PBLK; ++k)
-          *reinterpret_cast<uint4*>(pd + k * (kTile * 16)) =
-              make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
-        if (!seen) {
+        *reinterpret_cast<uint4*>(sm + G_::OFF_P + (j & 1) * G_::PBYTES + wg * (kTile * 16) + wt * 16) =
+            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        if (wg == 0 && !seen) {
           // a hidden row may hold NaN, and 0 NaN is not 0: clear its values
           const int slot = (2 * j + 1) % SLOTS;
           mbar_wait(&bar.full[slot], ((2 * j + 1) / SLOTS) & 1, &abort_s, c.status);
 #pragma unroll
           for (int k = 0; k < G_::RB / 16; ++k)
             *reinterpret_cast<uint4*>(sm + slot * G_::TILE + (k * 16 / G_::BW) * (kTile * G_::BW) +
-                                      tid * G_::BW + k * 16 % G_::BW) = make_uint4(0u, 0u, 0u, 0u);
+                                      wt * G_::BW + k * 16 % G_::BW) = make_uint4(0u, 0u, 0u, 0u);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
@@ -735,75 +769,69 @@ __global__ void __launch_bounds__(kThreads, Geo<E, D, F8, GP>::CTAS) paged_decod
         if (lane == 0) mbar_arrive(&bar.p_full[j & 1]);
       }
       // ------------------------------------------------ the segment's result
+      {  // l over the warp: lanes 8 h .. 8 h + 7 end with head h's sum
+        const bool hi = lane & 16, hj = lane & 8;
+        float a = hi ? l[2] : l[0], b = hi ? l[3] : l[1];
+        a += __shfl_xor_sync(0xffffffffu, hi ? l[0] : l[2], 16);
+        b += __shfl_xor_sync(0xffffffffu, hi ? l[1] : l[3], 16);
+        float t = hj ? b : a;
+        t += __shfl_xor_sync(0xffffffffu, hj ? a : b, 8);
 #pragma unroll
-      for (int h = 0; h < GP; ++h) {
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-        if (lane == 0) red_s[warp][h] = l[h];
+        for (int o = 4; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if ((lane & 7) == 0) red[ww][lane >> 3] = t;
       }
-      named_bar_sync(1, 128);
-      float acc[GP];
-      mbar_wait(&bar.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, &abort_s, c.status);
-      tc_fence_after();
-      {
-        uint32_t r[16];
-#pragma unroll
-        for (int c0 = 0; c0 < NP; c0 += 16) {
-          tmem_ld16(tm_o + c0 + my_lane, r);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int term = (c0 + k) / GP, h = (c0 + k) % GP;
-            const float v = __uint_as_float(r[k]);
-            if (term == 0) acc[h] = v;
-            else if (term < G_::PT)
-              acc[h] += v * (term == 1 ? 1.f / G_::TERM : 1.f / (G_::TERM * G_::TERM));
-          }
-        }
-      }
+      named_bar_sync(1 + wg, 128);
       const long long pair = (long long)w.b * c.Hkv + w.kvh;
       const bool final = w.cnt == w.seq.count;
-      // O^T's row of this thread (M = 64: sixteen rows a warp)
-      const int d = D == 128 ? tid : warp * 16 + lane;
-      const bool has_d = D == 128 || lane < 16;
       float* part = parts + (pair + blockIdx.x) * G * (D + 2);
-#pragma unroll
-      for (int h = 0; h < GP; ++h) {
-        if (h >= G) break;
-        const float m = ref_s[0][h];
-        const float lt = (red_s[0][h] + red_s[1][h]) + (red_s[2][h] + red_s[3][h]);
-        // O in units of 2^m
-        const float o = acc[h] * (F8 ? (ref_s[1][h] == -INFINITY
-                                            ? (m == -INFINITY ? 0.f : 1.f)
-                                            : fast_exp2(ref_s[1][h] - m - kBase))
-                                     : 0.015625f);
+      const long long row0 = (long long)w.b * p.Hq + w.kvh * G;
+      if (wt < H && h0 + wt < G) {
+        const int h = h0 + wt;
+        const float m = ref[0][wt], lt = (red[0][wt] + red[1][wt]) + (red[2][wt] + red[3][wt]);
+        // O is in units of 2^ref less the base (a head whose value scales are all 0
+        // has none, and an O of 0 or NaN)
+        const float mo = F8 ? ref[1][wt] : m;
+        float f;
         if (final) {
-          const long long row = (long long)w.b * p.Hq + w.kvh * G + h;
           const float a2 = sink_sm[seg & 7][h];
-          const float mt = fmaxf(m, a2), wt = ratio2(m, mt);
-          const float den = lt * wt + ratio2(a2, mt);
-          if (has_d)
-            static_cast<typename E::T*>(p.out)[row * D + d] =
-                (typename E::T)(den != 0.f ? o * wt / den : 0.f);
-          if (tid == h) {
-            p.lse[row] = den != 0.f ? (mt + log2f(den)) * kLn2 : -INFINITY;
-            if (p.sink_s) p.sink_s[row] = den != 0.f ? lt * wt / den : 0.f;
-          }
+          const float mt = fmaxf(m, a2);
+          const float lw = lt * ratio2(m, mt), den = lw + ratio2(a2, mt);
+          const float inv = den != 0.f ? 1.f / den : 0.f;
+          f = mo == -INFINITY ? inv : fast_exp2(mo - mt - kBase) * inv;
+          p.lse[row0 + h] = den != 0.f ? (mt + log2f(den)) * kLn2 : -INFINITY;
+          if (p.sink_s) p.sink_s[row0 + h] = lw * inv;
         } else {
-          if (has_d) part[h * (D + 2) + d] = o;
-          if (tid == h) {
-            part[h * (D + 2) + D] = m;
-            part[h * (D + 2) + D + 1] = lt;
-          }
+          f = mo == -INFINITY ? (m == -INFINITY ? 0.f : 1.f) : fast_exp2(mo - m - kBase);
+          part[h * (D + 2) + D] = m;
+          part[h * (D + 2) + D + 1] = lt;
+        }
+        fac_s[wg][wt] = f;
+      }
+      named_bar_sync(1 + wg, 128);
+      mbar_wait(&bar.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, &abort_s, c.status);
+      tc_fence_after();
+      uint32_t r[COLS];
+      tmem_ld(my_o, r);
+      tmem_ld_wait();
+      tc_fence_before();
+      // O^T's row of this thread (M = 64: sixteen rows a warp)
+      const int d = D == 128 ? wt : ww * 16 + lane;
+      if (D == 128 || lane < 16) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          if (h0 + h >= G) break;
+          float o = __uint_as_float(r[h]) + __uint_as_float(r[H + h]) * (1.f / G_::TERM);
+          if constexpr (G_::PT == 3) o += __uint_as_float(r[2 * H + h]) * (1.f / (G_::TERM * G_::TERM));
+          o *= fac_s[wg][h];
+          if (final) static_cast<typename E::T*>(p.out)[(row0 + h0 + h) * D + d] = (typename E::T)o;
+          else part[(h0 + h) * (D + 2) + d] = o;
         }
       }
-      tc_fence_before();
-      named_bar_sync(1, 128);  // the references and sums have been read
       ++seg;
     } while (w.next(p));
   }
   __syncthreads();
-  if (warp == 5) {
+  if (warp == W_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, G_::TMEM);
   }
@@ -872,9 +900,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodePro
   }
 }
 
-template <class E, int D, bool F8, int GP>
+template <class E, int D, bool F8, int NWG>
 int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
-  using G_ = Geo<E, D, F8, GP>;
+  using G_ = Geo<E, D, F8, NWG>;
   const PagedView& c = p.c;
   const int rows = c.n_pages * c.Hkv * c.page_size;
   CUtensorMap mk, mv;
@@ -883,7 +911,7 @@ int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
          : !make_tmap_3d(&mk, c.k_pages, rows, 1, D, 1, c.page_size) ||
                !make_tmap_3d(&mv, c.v_pages, rows, 1, D, 1, c.page_size))
     return SINKATTN_ERR_CUDA;
-  auto kern = paged_decode_kernel<E, D, F8, GP>;
+  auto kern = paged_decode_kernel<E, D, F8, NWG>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G_::SMEM) !=
       cudaSuccess)
     return SINKATTN_ERR_CUDA;
@@ -904,7 +932,7 @@ int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   cfg.stream = stream;
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(G_::THREADS);
   cfg.dynamicSmemBytes = G_::SMEM;
   const cudaError_t rc = cudaLaunchKernelEx(&cfg, kern, mk, mv, p);
   record_stop(SINKATTN_KERNEL_DECODE, stream);
@@ -920,9 +948,9 @@ int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
 template <class E, int D, bool F8>
 int decode_group(const PagedDecodeProblem& p, cudaStream_t stream) {
   const int G = p.Hq / p.c.Hkv;
-  if (G <= 4) return decode_cfg<E, D, F8, 4>(p, stream);
-  if (G <= 8) return decode_cfg<E, D, F8, 8>(p, stream);
-  return decode_cfg<E, D, F8, 16>(p, stream);
+  if (G <= kHeads) return decode_cfg<E, D, F8, 1>(p, stream);
+  if (G <= 2 * kHeads) return decode_cfg<E, D, F8, 2>(p, stream);
+  return decode_cfg<E, D, F8, 4>(p, stream);
 }
 template <class E, int D>
 int decode_typed(const PagedDecodeProblem& p, cudaStream_t stream) {
