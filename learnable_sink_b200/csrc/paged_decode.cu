@@ -86,7 +86,6 @@ struct Walk {
   }
   // a run that begins behind a pair's tiles begins with the next pair
   __device__ __forceinline__ bool begin(const PagedDecodeProblem& p) {
-    cut();
     return left > 0 && (cnt > 0 || next(p));
   }
   __device__ __forceinline__ bool next(const PagedDecodeProblem& p) {
@@ -118,13 +117,12 @@ __device__ __forceinline__ int cta_of(long long total, long long unit) {
 }
 
 struct Start {
-  int b;
-  long long base;   // units of one KV head before sequence b
-  long long total;  // units of all
+  Walk walk;
+  long long first, total;  // the run's first unit; units of all
 };
 
 // Adds up the lengths (a slice of the sequences a thread) and finds where this
-// CTA's run begins.
+// CTA's run begins; the thread whose slice it is in sets the walk up for all.
 template <int THREADS>
 __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* st, long long* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -147,18 +145,28 @@ __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* s
     total += s_warp[w];
   }
   total *= p.c.Hkv;
-  const long long x = quotient(run_begin(total, blockIdx.x), p.c.Hkv);  // units of one KV head
-  if (tid == 0) st->total = total;
-  if (x >= before && x < before + sum) {
-    int b = b0;
+  before *= p.c.Hkv;
+  const long long f0 = run_begin(total, blockIdx.x);
+  if (f0 >= before && f0 < before + sum * p.c.Hkv) {
+    Walk w;
+    w.b = b0;
     for (;;) {
-      const int c = seq_tiles(p, b).count + kPairUnits;
-      if (x < before + c) break;
-      before += c;
-      ++b;
+      w.seq = seq_tiles(p, w.b);
+      const long long units = (long long)(w.seq.count + kPairUnits) * p.c.Hkv;
+      if (f0 < before + units) break;
+      before += units;
+      ++w.b;
     }
-    st->b = b;
-    st->base = before;
+    const int rem = (int)(f0 - before), units = w.seq.count + kPairUnits;
+    w.kvh = rem / units;
+    w.t0 = rem - w.kvh * units;
+    w.left = run_begin(total, blockIdx.x + 1) - f0;
+    w.cut();
+    st->walk = w;
+    st->first = f0;
+    st->total = total;
+  } else if (f0 == total && tid == 0) {
+    st->walk.left = 0;  // less work than CTAs
   }
 }
 
@@ -373,20 +381,9 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   const uint32_t tmem = tmem_s;
   const uint32_t tm_s = tmem, tm_o = tmem + 2 * N;
 
-  const long long total = start_s.total;
-  const long long f0 = run_begin(total, blockIdx.x), run = run_begin(total, blockIdx.x + 1) - f0;
-  Walk w;
-  w.left = run;
-  bool work = w.left > 0;
-  if (work) {
-    w.b = start_s.b;
-    w.seq = seq_tiles(p, w.b);
-    const long long rem = f0 - start_s.base * c.Hkv;
-    const int units = w.seq.count + kPairUnits;
-    w.kvh = int(quotient(rem, units));
-    w.t0 = int(rem - (long long)w.kvh * units);
-    work = w.begin(p);
-  }
+  Walk w = start_s.walk;
+  const long long total = start_s.total, f0 = start_s.first, run = w.left;
+  const bool work = w.begin(p);
 
   if (!work) {
     // less work than CTAs
@@ -677,8 +674,8 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
 #pragma unroll
         for (int h = 0; h < H; ++h) {
           x[h] = seen ? x[h] : -INFINITY;
-          moves = moves || x[h] > ref[0][h] + kLag;
-          if constexpr (F8) moves = moves || x[h] + lvs > ref[1][h] + kLag;
+          moves |= x[h] > ref[0][h] + kLag;
+          if constexpr (F8) moves |= x[h] + lvs > ref[1][h] + kLag;
         }
         if (any_of_128(moves, wg)) {
           // rare: raise the references to the maxima so far, and bring l and O along
