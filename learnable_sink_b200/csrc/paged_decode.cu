@@ -42,7 +42,7 @@ namespace sk {
 
 namespace {
 
-constexpr int kTile = 128;     // positions per step
+constexpr int kRows = 128;     // rows of a K or V tile
 constexpr int kHeads = 4;      // query heads per softmax warpgroup
 constexpr int kMaxCtas = 320;
 
@@ -52,18 +52,19 @@ struct SeqTiles {
   int n, ts, f, count;
   __device__ __forceinline__ int tile(int i) const { return i < ts ? i : f + i - ts; }
 };
+template <int TP>  // positions per tile
 __device__ __forceinline__ SeqTiles seq_tiles(const PagedDecodeProblem& p, int b) {
   SeqTiles s;
   const int cap = p.c.max_pages << p.c.page_log2;
   s.n = min(max(__ldg(p.c.seqlens + b), 0), cap);
-  const int all = s.n / kTile + (s.n % kTile != 0);
+  const int all = s.n / TP + (s.n % TP != 0);
   s.ts = max(all, 1);  // a pair without a key still has a (masked) tile, which writes its result
   s.f = 0;
   s.count = s.ts;
   const int w0 = s.n - p.window;
   if (p.window > 0 && w0 > p.n_sink) {
-    s.ts = p.n_sink / kTile + (p.n_sink % kTile != 0);
-    s.f = max(w0 / kTile, s.ts);
+    s.ts = p.n_sink / TP + (p.n_sink % TP != 0);
+    s.f = max(w0 / TP, s.ts);
     s.count = s.ts + all - s.f;
   }
   return s;
@@ -77,6 +78,7 @@ __device__ __forceinline__ bool visible(const PagedDecodeProblem& p, int n, int 
 constexpr int kPairUnits = 1;
 
 // A CTA's run of units, walked segment by segment (every role walks for itself).
+template <int TP>
 struct Walk {
   int b, kvh, t0, cnt;  // the segment: tiles [t0, t0 + cnt) of (b, kvh)
   SeqTiles seq;
@@ -94,7 +96,7 @@ struct Walk {
     t0 = 0;
     if (++kvh == p.c.Hkv) {
       kvh = 0;
-      seq = seq_tiles(p, ++b);
+      seq = seq_tiles<TP>(p, ++b);
     }
     cut();
     return true;
@@ -116,20 +118,22 @@ __device__ __forceinline__ int cta_of(long long total, long long unit) {
   return (int)quotient((unit + 1) * n - 1, total);
 }
 
+template <int TP>
 struct Start {
-  Walk walk;
+  Walk<TP> walk;
   long long first, total;  // the run's first unit; units of all
 };
 
 // Adds up the lengths (a slice of the sequences a thread) and finds where this
 // CTA's run begins; the thread whose slice it is in sets the walk up for all.
-template <int THREADS>
-__device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* st, long long* s_warp) {
+template <int THREADS, int TP>
+__device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start<TP>* st,
+                                           long long* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per_thread = (p.c.B + THREADS - 1) / THREADS;
   const int b0 = tid * per_thread, b1 = min(b0 + per_thread, p.c.B);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += seq_tiles(p, b).count + kPairUnits;
+  for (int b = b0; b < b1; ++b) sum += seq_tiles<TP>(p, b).count + kPairUnits;
   long long inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -148,10 +152,10 @@ __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* s
   before *= p.c.Hkv;
   const long long f0 = run_begin(total, blockIdx.x);
   if (f0 >= before && f0 < before + sum * p.c.Hkv) {
-    Walk w;
+    Walk<TP> w;
     w.b = b0;
     for (;;) {
-      w.seq = seq_tiles(p, w.b);
+      w.seq = seq_tiles<TP>(p, w.b);
       const long long units = (long long)(w.seq.count + kPairUnits) * p.c.Hkv;
       if (f0 < before + units) break;
       before += units;
@@ -175,21 +179,29 @@ __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* s
 template <class E, int D, bool F8, int NWG>
 struct Geo {
   static constexpr int EB = F8 ? 1 : 2;
-  static constexpr int RB = D * EB;                    // bytes of a row
-  static constexpr int BW = RB < 128 ? RB : 128;       // of a TMA box's row
+  static constexpr int CB = D * EB;                    // bytes of a position
+  // Positions per row of a tile: a copy takes about 4.5 cycles for a row of up to
+  // 128 bytes, so two positions of 64 bytes, neighbours in memory, share one; K's
+  // halves are then multiplied apart, into columns of their own, and V's half rows
+  // with the probabilities of their own positions (a StreamingLLM band: 25 -> XX us).
+  static constexpr int PP = CB == 64 ? 2 : 1;
+  static constexpr int TP = kRows * PP;                // positions per tile
+  static constexpr int RB = CB * PP;                   // bytes of a row
+  static constexpr int BW = 128;                       // of a TMA box's row
   static constexpr int NB = RB / BW;                   // boxes per row
-  static constexpr int TILE = kTile * RB;              // K or V tile
+  static constexpr int QW = CB < 128 ? CB : 128;       // width of a query's rows
+  static constexpr int TILE = kRows * RB;              // K or V tile
   static constexpr int QT = F8 ? (E::kFmt == 0 ? 3 : 2) : 1;  // terms of a query
   static constexpr int PT = F8 ? 3 : 2;                // terms of a probability
   // A warpgroup's columns: term t of head h at 4 t + h of 16 bytes' worth, so that
   // a thread's probabilities are one 16-byte store.
   static constexpr int COLS = 16 / EB;
-  static constexpr int N = COLS * NWG < 16 ? 16 : COLS * NWG;  // columns of S^T and O^T
-  static constexpr int PBLK = N / COLS;                // 16-byte units per position
-  static constexpr int PBYTES = PBLK * kTile * 16;
-  static constexpr int QBYTES = N * RB;
+  static constexpr int N = COLS * NWG < 16 ? 16 : COLS * NWG;  // of the queries
+  static constexpr int NT = N * PP;                    // columns of S^T and of O^T
+  static constexpr int PBYTES = NT / COLS * kRows * 16;
+  static constexpr int QBYTES = N * CB;
   static constexpr int KE = 32 / EB;                   // K extent of an instruction
-  static constexpr int TMEM = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 256;
+  static constexpr int TMEM = 3 * NT <= 64 ? 64 : 3 * NT <= 128 ? 128 : 3 * NT <= 256 ? 256 : 512;
   static constexpr int WARPS = 4 * NWG + 4, THREADS = WARPS * 32;
   // CTAs an SM: one's segment ends and waits overlap the other's work.  32 KB tiles
   // (or sixteen heads) leave room for one.
@@ -240,12 +252,12 @@ __device__ __forceinline__ uint64_t sdesc_rows(uint32_t addr, uint32_t lbo) {
   return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
          (uint64_t((BW * 8) >> 4) << 32) | (uint64_t(1) << 46) | (type << 61);
 }
-// P: position k's 16-byte unit i at i 2048 + 16 k, no swizzle: 8-position groups
-// 128 bytes apart, units 2048.  A thread stores its position with one vector
-// store a unit, free of bank conflicts.
+// P: row k's 16-byte unit i at i 2048 + 16 k, no swizzle: 8-row groups 128 bytes
+// apart, units 2048.  A thread stores a position with one vector store, free of
+// bank conflicts.
 __device__ __forceinline__ uint64_t sdesc_p(uint32_t addr) {
   return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t(128 >> 4) << 16) |
-         (uint64_t((kTile * 16) >> 4) << 32) | (uint64_t(1) << 46);
+         (uint64_t((kRows * 16) >> 4) << 32) | (uint64_t(1) << 46);
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -318,7 +330,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
                         const __grid_constant__ CUtensorMap tmap_v,
                         const __grid_constant__ PagedDecodeProblem p) {
   using G_ = Geo<E, D, F8, NWG>;
-  constexpr int SLOTS = G_::SLOTS, N = G_::N, COLS = G_::COLS, GP = NWG * kHeads, H = kHeads;
+  constexpr int SLOTS = G_::SLOTS, N = G_::N, NT = G_::NT, PP = G_::PP, TP = G_::TP, COLS = G_::COLS, GP = NWG * kHeads, H = kHeads;
   constexpr int W_TMA = 4 * NWG, W_MMA = W_TMA + 1, W_Q = W_TMA + 2;
   extern __shared__ uint8_t dsm_raw[];
   uint8_t* sm =
@@ -326,7 +338,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   __shared__ Bars<SLOTS> bar;
   __shared__ int abort_s;
   __shared__ uint32_t tmem_s;
-  __shared__ Start start_s;
+  __shared__ Start<TP> start_s;
   __shared__ long long warp_s[G_::WARPS];
   __shared__ __align__(16) float qs_s[8][GP];  // query scales of the last eight segments
   __shared__ float sink_sm[8][GP];             // their sink logits, log2 units
@@ -338,7 +350,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   // the result.
   __shared__ __align__(16) float ref_s[NWG][2][H], corr_s[NWG][2][H], red_s[NWG][4][2 * H], fac_s[NWG][H];
   // a tile's pages: score factor and log2 of the value scale (NaN: outside the pool)
-  __shared__ float2 page_s[2][8];
+  __shared__ float2 page_s[2][TP / 16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.Hq / p.c.Hkv;
   const PagedView& c = p.c;
@@ -373,15 +385,15 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   // up to here nothing that another kernel writes was read: this kernel is itself
   // a programmatic dependent, and its start lies under the end of the last one
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  find_start<G_::THREADS>(p, &start_s, warp_s);
+  find_start<G_::THREADS, TP>(p, &start_s, warp_s);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = tmem_s;
-  const uint32_t tm_s = tmem, tm_o = tmem + 2 * N;
+  const uint32_t tm_s = tmem, tm_o = tmem + 2 * NT;
 
-  Walk w = start_s.walk;
+  Walk<TP> w = start_s.walk;
   const long long total = start_s.total, f0 = start_s.first, run = w.left;
   const bool work = w.begin(p);
 
@@ -389,25 +401,32 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
     // less work than CTAs
   } else if (warp == W_TMA) {
     // ---------------------------------------------------------------- TMA
-    const int ppt_log2 = 7 - c.page_log2, ppt = 1 << ppt_log2;  // pages per tile
-    int ld = 0;                                                 // tiles (K or V) issued
+    const int ppt = TP >> c.page_log2;  // pages per tile
+    int ld = 0;                         // tiles (K or V) issued
     bool ok = true;
     do {
-      for (int i = 0; i < w.cnt && ok; ++i) {
-        const int page0 = w.seq.tile(w.t0 + i) << ppt_log2;
+      auto load_id = [&](int i) {  // lane's page of tile i, -1: none to bring
         int id = -1;
-        if (lane < ppt) {
-          const int pos = (page0 + lane) << c.page_log2;
+        if (lane < ppt && i < w.cnt) {
+          const int page = w.seq.tile(w.t0 + i) * ppt + lane;
+          const int pos = page << c.page_log2;
           if (pos < w.seq.n && (p.window <= 0 || pos < p.n_sink ||
                                 pos + c.page_size > w.seq.n - p.window))
-            id = __ldg(c.table + (long long)w.b * c.max_pages + page0 + lane);
+            id = __ldg(c.table + (long long)w.b * c.max_pages + page);
           if (id >= c.n_pages) id = -1;
         }
+        return id;
+      };
+      int next = load_id(0);
+      for (int i = 0; i < w.cnt && ok; ++i) {
+        const int id = next;
+        next = load_id(i + 1);
         const uint32_t need = __ballot_sync(0xffffffffu, id >= 0);
-        const uint32_t bytes = __popc(need) * (uint32_t)(c.page_size * G_::RB);
+        const uint32_t bytes = __popc(need) * (uint32_t)(c.page_size * G_::CB);
         const int src = lane / G_::NB, nb = lane % G_::NB;  // this lane's page and box
         const int my = __shfl_sync(0xffffffffu, id, src);
-        const int row = (my * c.Hkv + w.kvh) << c.page_log2;
+        const int row = ((my * c.Hkv + w.kvh) << c.page_log2) / PP;
+        const int at = nb * (kRows * G_::BW) + (src << c.page_log2) / PP * G_::BW;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++ld) {
           const int slot = ld % SLOTS;
@@ -417,9 +436,8 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
           if (lane == 0) mbar_expect_tx(&bar.full[slot], bytes);
           __syncwarp();
           if (src < ppt && my >= 0)
-            tma_load_3d(sm + slot * G_::TILE + nb * (kTile * G_::BW) +
-                            (src << c.page_log2) * G_::BW,
-                        kv ? &tmap_v : &tmap_k, &bar.full[slot], nb * (G_::BW / G_::EB), 0, row);
+            tma_load_3d(sm + slot * G_::TILE + at, kv ? &tmap_v : &tmap_k, &bar.full[slot],
+                        nb * (G_::BW / G_::EB), 0, row);
         }
       }
     } while (ok && w.next(p));
@@ -443,12 +461,12 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
              mbar_wait(&bar.full[slot], ((2 * pend + 1) / SLOTS) & 1, &abort_s, c.status);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t ad = sdesc_rows<G_::BW>(base + slot * G_::TILE, kTile * G_::BW);
+        const uint64_t ad = sdesc_rows<G_::BW>(base + slot * G_::TILE, kRows * G_::BW);
         const uint64_t bd = sdesc_p(base + G_::OFF_P + (pend & 1) * G_::PBYTES);
 #pragma unroll
-        for (int k = 0; k < kTile / G_::KE; ++k)
+        for (int k = 0; k < kRows / G_::KE; ++k)
           mma<F8>(tm_o, sdesc_add(ad, k * G_::KE * G_::BW), sdesc_add(bd, k * G_::KE * 16),
-                  idesc<E, F8>(D, N, 1, 1), k > 0 || !pend_first);
+                  idesc<E, F8>(D * PP, NT, 1, 1), k > 0 || !pend_first);
         mma_commit(&bar.empty[slot]);
         mma_commit(&bar.pv_done[pend & 1]);
         pend = -1;
@@ -463,13 +481,17 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
           if (!ok) break;
           tc_fence_after();
           const uint64_t ad = sdesc_rows<G_::BW>(base + slot * G_::TILE, 16);
-          const uint64_t bd = sdesc_rows<G_::BW>(base + G_::OFF_Q + (seg & 1) * G_::QBYTES, 16);
+          const uint64_t bd = sdesc_rows<G_::QW>(base + G_::OFF_Q + (seg & 1) * G_::QBYTES, 16);
 #pragma unroll
-          for (int k = 0; k < G_::RB / 32; ++k) {
-            const int box = k * 32 / G_::BW, in = k * 32 % G_::BW;
-            mma<F8>(tm_s + (j & 1) * N, sdesc_add(ad, box * kTile * G_::BW + in),
-                    sdesc_add(bd, box * N * G_::BW + in), idesc<E, F8>(kTile, N, 0, 0), k > 0);
-          }
+          for (int q = 0; q < PP; ++q)
+#pragma unroll
+            for (int k = 0; k < G_::CB / 32; ++k) {
+              const int a_at = q * G_::CB + k * 32, b_at = k * 32;
+              mma<F8>(tm_s + (j & 1) * NT + q * N,
+                      sdesc_add(ad, a_at / G_::BW * kRows * G_::BW + a_at % G_::BW),
+                      sdesc_add(bd, b_at / G_::QW * N * G_::QW + b_at % G_::QW),
+                      idesc<E, F8>(kRows, N, 0, 0), k > 0);
+            }
           mma_commit(&bar.empty[slot]);
           mma_commit(&bar.s_full[j & 1]);
           if (i == w.cnt - 1) mma_commit(&bar.q_free[seg & 1]);
@@ -499,9 +521,9 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       const typename E::T* q =
           static_cast<const typename E::T*>(p.q) + ((long long)w.b * p.Hq + w.kvh * G) * D + lane * CPL;
       auto at = [&](int r, int byte) {  // row r of the block, swizzled as the tiles are
-        const int box = byte / G_::BW, in = byte % G_::BW, ch = in >> 4;
-        const int x = G_::BW == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
-        return qd + box * (N * G_::BW) + r * G_::BW + (x << 4) + (in & 15);
+        const int box = byte / G_::QW, in = byte % G_::QW, ch = in >> 4;
+        const int x = G_::QW == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
+        return qd + box * (N * G_::QW) + r * G_::QW + (x << 4) + (in & 15);
       };
       uint32_t raws[GP][CPL / 2];
 #pragma unroll
@@ -577,7 +599,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
     } while (w.next(p));
   } else if (warp == W_Q + 1) {
     // ---------------------------------------------------------------- page scales
-    const int ppt_log2 = 7 - c.page_log2, ppt = 1 << ppt_log2;
+    const int ppt = TP >> c.page_log2;
     const float scale_log2 = p.scale * kLog2e;
     int j = 0;
     bool ok = true;
@@ -585,7 +607,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       auto load_id = [&](int i) {
         int id = -2;  // no visible position
         if (lane < ppt && i < w.cnt) {
-          const int page = (w.seq.tile(w.t0 + i) << ppt_log2) + lane;
+          const int page = w.seq.tile(w.t0 + i) * ppt + lane;
           const int pos = page << c.page_log2;
           if (pos < w.seq.n && (p.window <= 0 || pos < p.n_sink ||
                                 pos + c.page_size > w.seq.n - p.window)) {
@@ -645,47 +667,56 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       for (int h = 0; h < H; ++h) l[h] = 0.f;
       if (wt < 2 * H) ref[wt / H][wt % H] = -INFINITY;
       for (int i = 0; i < w.cnt; ++i, ++j) {
-        const int pos = w.seq.tile(w.t0 + i) * kTile + wt;
+        const int pos0 = w.seq.tile(w.t0 + i) * TP + wt * PP;
         mbar_wait(&bar.s_full[j & 1], (j >> 1) & 1, &abort_s, c.status);
         tc_fence_after();
-        const float2 page = page_s[j & 1][wt >> c.page_log2];
-        const bool seen = visible(p, w.seq.n, pos) && !isnan(page.y);
-        const float lvs = seen ? page.y : 0.f;
+        const float2 page = page_s[j & 1][wt * PP >> c.page_log2];
+        const bool held = !isnan(page.y);
+        const float lvs = held ? page.y : 0.f;
         // scores in log2 units; hidden positions at -inf whatever their rows hold
-        float x[H];
+        bool seen[PP];
+        float x[PP][H];
         if constexpr (F8) {
-          uint32_t r[16];
-          tmem_ld(my_s + (j & 1) * N, r);
+          uint32_t r[PP][16];
+#pragma unroll
+          for (int q = 0; q < PP; ++q) tmem_ld(my_s + (j & 1) * NT + q * N, r[q]);
           tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < H; ++h) {
-            x[h] = __uint_as_float(r[h]) + __uint_as_float(r[H + h]) * 0.0625f;
-            if constexpr (G_::QT == 3) x[h] += __uint_as_float(r[2 * H + h]) * 0.00390625f;
-            x[h] *= page.x * qs_s[seg & 7][h0 + h];
-          }
+          for (int q = 0; q < PP; ++q)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              x[q][h] = __uint_as_float(r[q][h]) + __uint_as_float(r[q][H + h]) * 0.0625f;
+              if constexpr (G_::QT == 3) x[q][h] += __uint_as_float(r[q][2 * H + h]) * 0.00390625f;
+              x[q][h] *= page.x * qs_s[seg & 7][h0 + h];
+            }
         } else {
           uint32_t r[4];
-          tmem_ld(my_s + (j & 1) * N, r);
+          tmem_ld(my_s + (j & 1) * NT, r);
           tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < H; ++h) x[h] = __uint_as_float(r[h]) * page.x;
+          for (int h = 0; h < H; ++h) x[0][h] = __uint_as_float(r[h]) * page.x;
         }
         bool moves = i == 0;
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-          x[h] = seen ? x[h] : -INFINITY;
-          moves |= x[h] > ref[0][h] + kLag;
-          if constexpr (F8) moves |= x[h] + lvs > ref[1][h] + kLag;
+        for (int q = 0; q < PP; ++q) {
+          seen[q] = held && visible(p, w.seq.n, pos0 + q);
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            x[q][h] = seen[q] ? x[q][h] : -INFINITY;
+            moves |= x[q][h] > ref[0][h] + kLag;
+            if constexpr (F8) moves |= x[q][h] + lvs > ref[1][h] + kLag;
+          }
         }
         if (any_of_128(moves, wg)) {
           // rare: raise the references to the maxima so far, and bring l and O along
           float mine = 0.f;
 #pragma unroll
           for (int h = 0; h < H; ++h) {
-            const float a = warp_max(x[h]);
+            const float xm = PP == 2 ? fmaxf(x[0][h], x[PP - 1][h]) : x[0][h];
+            const float a = warp_max(xm);
             mine = lane == h ? a : mine;
             if constexpr (F8) {
-              const float b = warp_max(x[h] + lvs);
+              const float b = warp_max(xm + lvs);
               mine = lane == H + h ? b : mine;
             }
           }
@@ -703,62 +734,72 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
           if (i > 0) {
             mbar_wait(&bar.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, &abort_s, c.status);
             tc_fence_after();
-            uint32_t r[COLS];
-            tmem_ld(my_o, r);
-            tmem_ld_wait();
 #pragma unroll
             for (int h = 0; h < H; ++h) l[h] *= corr[0][h];
 #pragma unroll
-            for (int k = 0; k < COLS; ++k)
-              r[k] = __float_as_uint(__uint_as_float(r[k]) * corr[F8][k % H]);
-            tmem_st(my_o, r);
+            for (int q = 0; q < PP; ++q) {
+              uint32_t r[COLS];
+              tmem_ld(my_o + q * N, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < COLS; ++k)
+                r[k] = __float_as_uint(__uint_as_float(r[k]) * corr[F8][k % H]);
+              tmem_st(my_o + q * N, r);
+            }
             tmem_st_wait();
           }
         }
         // P's buffer is free: the commit behind these scores covers the products
         // issued before them, P V of two tiles ago among them
-        uint32_t pk[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int h = 0; h < H; h += 2) {
-          float e[2];
+        for (int q = 0; q < PP; ++q) {
+          uint32_t pk[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float pr = x[h + k] == -INFINITY ? 0.f : fast_exp2(x[h + k] - ref[0][h + k]);
-            l[h + k] += pr;
-            if constexpr (F8) {
-              const float y = x[h + k] + lvs;
-              e[k] = y == -INFINITY ? 0.f : fast_exp2(y - ref[1][h + k] + kBase);
-            } else {
-              e[k] = pr * 64.f;
+          for (int h = 0; h < H; h += 2) {
+            float e[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float xk = x[q][h + k];
+              const float pr = xk == -INFINITY ? 0.f : fast_exp2(xk - ref[0][h + k]);
+              l[h + k] += pr;
+              if constexpr (F8) {
+                const float y = xk + lvs;
+                e[k] = y == -INFINITY ? 0.f : fast_exp2(y - ref[1][h + k] + kBase);
+              } else {
+                e[k] = pr * 64.f;
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < G_::PT; ++t) {
+              if constexpr (F8) {
+                const uint32_t two = e4m3x2(e[0], e[1]);
+                const float2 v = e4m3x2_value(two);
+                pk[t] |= two << (8 * h);
+                e[0] = (e[0] - v.x) * G_::TERM;
+                e[1] = (e[1] - v.y) * G_::TERM;
+              } else {
+                const uint32_t two = E::pack(e[0], e[1]);
+                const float2 v = E::widen(two);
+                pk[2 * t + h / 2] = two;
+                e[0] = (e[0] - v.x) * G_::TERM;
+                e[1] = (e[1] - v.y) * G_::TERM;
+              }
             }
           }
-#pragma unroll
-          for (int t = 0; t < G_::PT; ++t) {
-            if constexpr (F8) {
-              const uint32_t two = e4m3x2(e[0], e[1]);
-              const float2 v = e4m3x2_value(two);
-              pk[t] |= two << (8 * h);
-              e[0] = (e[0] - v.x) * G_::TERM;
-              e[1] = (e[1] - v.y) * G_::TERM;
-            } else {
-              const uint32_t two = E::pack(e[0], e[1]);
-              const float2 v = E::widen(two);
-              pk[2 * t + h / 2] = two;
-              e[0] = (e[0] - v.x) * G_::TERM;
-              e[1] = (e[1] - v.y) * G_::TERM;
-            }
-          }
+          *reinterpret_cast<uint4*>(sm + G_::OFF_P + (j & 1) * G_::PBYTES +
+                                    (q * (N / COLS) + wg) * (kRows * 16) + wt * 16) =
+              make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
-        *reinterpret_cast<uint4*>(sm + G_::OFF_P + (j & 1) * G_::PBYTES + wg * (kTile * 16) + wt * 16) =
-            make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        if (wg == 0 && !seen) {
+        if (wg == 0 && (!seen[0] || !seen[PP - 1])) {
           // a hidden row may hold NaN, and 0 NaN is not 0: clear its values
           const int slot = (2 * j + 1) % SLOTS;
           mbar_wait(&bar.full[slot], ((2 * j + 1) / SLOTS) & 1, &abort_s, c.status);
+          uint8_t* row = sm + slot * G_::TILE + wt * G_::BW;
 #pragma unroll
           for (int k = 0; k < G_::RB / 16; ++k)
-            *reinterpret_cast<uint4*>(sm + slot * G_::TILE + (k * 16 / G_::BW) * (kTile * G_::BW) +
-                                      wt * G_::BW + k * 16 % G_::BW) = make_uint4(0u, 0u, 0u, 0u);
+            if (!seen[k * 16 / G_::CB])  // 16-byte unit k of the row, where the swizzle puts it
+              *reinterpret_cast<uint4*>(row + k / 8 * (kRows * G_::BW) + ((k % 8 ^ (wt & 7)) << 4)) =
+                  make_uint4(0u, 0u, 0u, 0u);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
@@ -807,21 +848,40 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       named_bar_sync(1 + wg, 128);
       mbar_wait(&bar.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, &abort_s, c.status);
       tc_fence_after();
+      // O^T's row of this thread.  M = 64 has sixteen rows a warp; with two positions
+      // a row, rows 64 to 127 are the second ones' (in columns of their own), and come
+      // to the first ones' threads through this warpgroup's part of a P buffer.
       uint32_t r[COLS];
-      tmem_ld(my_o, r);
+      tmem_ld(my_o + (PP == 2 ? (ww >> 1) * N : 0), r);
       tmem_ld_wait();
       tc_fence_before();
-      // O^T's row of this thread (M = 64: sixteen rows a warp)
-      const int d = D == 128 ? wt : ww * 16 + lane;
-      if (D == 128 || lane < 16) {
+      float o[H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        o[h] = __uint_as_float(r[h]) + __uint_as_float(r[H + h]) * (1.f / G_::TERM);
+        if constexpr (G_::PT == 3)
+          o[h] += __uint_as_float(r[2 * H + h]) * (1.f / (G_::TERM * G_::TERM));
+      }
+      if constexpr (PP == 2) {
+        float4* half = reinterpret_cast<float4*>(sm + G_::OFF_P + wg * (kRows * 16)) + (wt & 63);
+        if (wt >= 64) *half = make_float4(o[0], o[1], o[2], o[3]);
+        named_bar_sync(1 + wg, 128);
+        if (wt < 64) {
+          const float4 v = *half;
+          o[0] += v.x;
+          o[1] += v.y;
+          o[2] += v.z;
+          o[3] += v.w;
+        }
+      }
+      const int d = D == 128 || PP == 2 ? wt : ww * 16 + lane;
+      if (D == 128 || (PP == 2 ? wt < 64 : lane < 16)) {
 #pragma unroll
         for (int h = 0; h < H; ++h) {
           if (h0 + h >= G) break;
-          float o = __uint_as_float(r[h]) + __uint_as_float(r[H + h]) * (1.f / G_::TERM);
-          if constexpr (G_::PT == 3) o += __uint_as_float(r[2 * H + h]) * (1.f / (G_::TERM * G_::TERM));
-          o *= fac_s[wg][h];
-          if (final) static_cast<typename E::T*>(p.out)[(row0 + h0 + h) * D + d] = (typename E::T)o;
-          else part[(h0 + h) * (D + 2) + d] = o;
+          const float v = o[h] * fac_s[wg][h];
+          if (final) static_cast<typename E::T*>(p.out)[(row0 + h0 + h) * D + d] = (typename E::T)v;
+          else part[(h0 + h) * (D + 2) + d] = v;
         }
       }
       ++seg;
@@ -903,8 +963,9 @@ int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
   const PagedView& c = p.c;
   const int rows = c.n_pages * c.Hkv * c.page_size;
   CUtensorMap mk, mv;
-  if (F8 ? !make_tmap_codes(&mk, c.k_pages, rows, 1, D, c.page_size) ||
-               !make_tmap_codes(&mv, c.v_pages, rows, 1, D, c.page_size)
+  constexpr int PP = G_::PP;
+  if (F8 ? !make_tmap_codes(&mk, c.k_pages, rows / PP, 1, D * PP, c.page_size / PP) ||
+               !make_tmap_codes(&mv, c.v_pages, rows / PP, 1, D * PP, c.page_size / PP)
          : !make_tmap_3d(&mk, c.k_pages, rows, 1, D, 1, c.page_size) ||
                !make_tmap_3d(&mv, c.v_pages, rows, 1, D, 1, c.page_size))
     return SINKATTN_ERR_CUDA;
@@ -916,7 +977,7 @@ int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // no more CTAs than the tables have tiles
-  const long long tiles = ((long long)c.max_pages * c.page_size + kTile - 1) / kTile;
+  const long long tiles = ((long long)c.max_pages * c.page_size + G_::TP - 1) / G_::TP;
   long long grid = tiles * c.B * c.Hkv;
   if (grid > G_::CTAS * sms) grid = G_::CTAS * sms;
   if (grid > kMaxCtas) grid = kMaxCtas;
