@@ -223,7 +223,10 @@ struct Geo {
 };
 
 // Probabilities are held as 2^kBase e^{x - m}: with a reference that lags by at
-// most 2^kLag they stay within 2^8 (E4M3 reaches 448), as high as they can.
+// most 2^kLag they stay within 2^8 (E4M3 reaches 448), as high as they can.  The
+// 8-bit terms are split in f16 pairs: its eleven bits are what three terms hold, a
+// residue and its move by 2^5 are exact in it, and it takes half the instructions
+// of float32 (its last bit, 2^-24, lies below the third term's, 2^-20).
 constexpr float kLag = 2.f, kBase = 6.f;
 
 template <bool F8>
@@ -260,6 +263,13 @@ __device__ __forceinline__ uint64_t sdesc_p(uint32_t addr) {
          (uint64_t((kRows * 16) >> 4) << 32) | (uint64_t(1) << 46);
 }
 
+// the same between E4M3 pairs and f16 pairs
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(__half2 v) {
+  return __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ __half2 f16x2_of_e4m3x2(uint32_t two) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3));
+}
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
@@ -307,6 +317,9 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
+// The reference of a row that has seen nothing: low enough that every score
+// raises it, and finite, so that -inf minus it is -inf and not NaN.
+constexpr float kNone = -3e38f;
 // 2^(a - b), 0 from a = -inf (also over b = -inf)
 __device__ __forceinline__ float ratio2(float a, float b) {
   return a == -INFINITY ? 0.f : fast_exp2(a - b);
@@ -665,7 +678,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       float l[H];
 #pragma unroll
       for (int h = 0; h < H; ++h) l[h] = 0.f;
-      if (wt < 2 * H) ref[wt / H][wt % H] = -INFINITY;
+      if (wt < 2 * H) ref[wt / H][wt % H] = kNone;
       for (int i = 0; i < w.cnt; ++i, ++j) {
         const int pos0 = w.seq.tile(w.t0 + i) * TP + wt * PP;
         mbar_wait(&bar.s_full[j & 1], (j >> 1) & 1, &abort_s, c.status);
@@ -682,13 +695,15 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
           for (int q = 0; q < PP; ++q) tmem_ld(my_s + (j & 1) * NT + q * N, r[q]);
           tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < PP; ++q)
+          for (int h = 0; h < H; ++h) {
+            const float f = page.x * qs_s[seg & 7][h0 + h];
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-              x[q][h] = __uint_as_float(r[q][h]) + __uint_as_float(r[q][H + h]) * 0.0625f;
-              if constexpr (G_::QT == 3) x[q][h] += __uint_as_float(r[q][2 * H + h]) * 0.00390625f;
-              x[q][h] *= page.x * qs_s[seg & 7][h0 + h];
+            for (int q = 0; q < PP; ++q) {
+              float v = __uint_as_float(r[q][H + h]);
+              if constexpr (G_::QT == 3) v += __uint_as_float(r[q][2 * H + h]) * 0.0625f;
+              x[q][h] = (__uint_as_float(r[q][h]) + v * 0.0625f) * f;
             }
+          }
         } else {
           uint32_t r[4];
           tmem_ld(my_s + (j & 1) * NT, r);
@@ -703,8 +718,8 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
 #pragma unroll
           for (int h = 0; h < H; ++h) {
             x[q][h] = seen[q] ? x[q][h] : -INFINITY;
-            moves |= x[q][h] > ref[0][h] + kLag;
-            if constexpr (F8) moves |= x[q][h] + lvs > ref[1][h] + kLag;
+            moves |= x[q][h] - ref[0][h] > kLag;
+            if constexpr (F8) moves |= x[q][h] + (lvs - ref[1][h]) > kLag;
           }
         }
         if (any_of_128(moves, wg)) {
@@ -759,25 +774,22 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
             float e[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float xk = x[q][h + k];
-              const float pr = xk == -INFINITY ? 0.f : fast_exp2(xk - ref[0][h + k]);
+              const float pr = fast_exp2(x[q][h + k] - ref[0][h + k]);
               l[h + k] += pr;
-              if constexpr (F8) {
-                const float y = xk + lvs;
-                e[k] = y == -INFINITY ? 0.f : fast_exp2(y - ref[1][h + k] + kBase);
-              } else {
-                e[k] = pr * 64.f;
-              }
+              e[k] = F8 ? fast_exp2(x[q][h + k] + (lvs - ref[1][h + k] + kBase)) : pr * 64.f;
             }
+            if constexpr (F8) {
+              __half2 v = __floats2half2_rn(e[0], e[1]);
 #pragma unroll
-            for (int t = 0; t < G_::PT; ++t) {
-              if constexpr (F8) {
-                const uint32_t two = e4m3x2(e[0], e[1]);
-                const float2 v = e4m3x2_value(two);
+              for (int t = 0; t < G_::PT; ++t) {
+                const uint32_t two = e4m3x2_of_f16x2(v);
                 pk[t] |= two << (8 * h);
-                e[0] = (e[0] - v.x) * G_::TERM;
-                e[1] = (e[1] - v.y) * G_::TERM;
-              } else {
+                if (t + 1 < G_::PT)
+                  v = __hmul2(__hsub2(v, f16x2_of_e4m3x2(two)), __float2half2_rn(G_::TERM));
+              }
+            } else {
+#pragma unroll
+              for (int t = 0; t < G_::PT; ++t) {
                 const uint32_t two = E::pack(e[0], e[1]);
                 const float2 v = E::widen(two);
                 pk[2 * t + h / 2] = two;
@@ -835,11 +847,11 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
           const float mt = fmaxf(m, a2);
           const float lw = lt * ratio2(m, mt), den = lw + ratio2(a2, mt);
           const float inv = den != 0.f ? 1.f / den : 0.f;
-          f = mo == -INFINITY ? inv : fast_exp2(mo - mt - kBase) * inv;
+          f = mo == kNone ? inv : fast_exp2(mo - mt - kBase) * inv;
           p.lse[row0 + h] = den != 0.f ? (mt + log2f(den)) * kLn2 : -INFINITY;
           if (p.sink_s) p.sink_s[row0 + h] = lw * inv;
         } else {
-          f = mo == -INFINITY ? (m == -INFINITY ? 0.f : 1.f) : fast_exp2(mo - m - kBase);
+          f = mo == kNone ? 1.f : fast_exp2(mo - m - kBase);
           part[h * (D + 2) + D] = m;
           part[h * (D + 2) + D + 1] = lt;
         }
