@@ -502,7 +502,8 @@ int sinkattn_paged_append_fp8(sinkattn_dtype dt, int T, int Hq, const sinkattn_p
  * visible if j < cache_seqlens[b] and, with window > 0, j < n_sink or
  * j >= cache_seqlens[b] - window (the StreamingLLM set; pages wholly outside it
  * are not read).
- *   q              [B, Hq, D] of type dt; Hq / Hkv from 1 to 16 (above:
+ *   q              [B, Hq, D] of type dt; Hq / Hkv from 1 to 16, and
+ *                  B Hkv (max_pages page_size / 128 + 2) below 2^31 (else
  *                  UNSUPPORTED).
  *   learnable_sink, out, lse_new, sink_s  as for sinkattn_decode.  A sequence
  *                  that sees no key gets out = 0, lse = a_h (-inf without a

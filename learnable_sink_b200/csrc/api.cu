@@ -537,6 +537,7 @@ int paged_decode(bool fp8, sinkattn_dtype dt, int Hq, float scale, const void* q
   const int rc = paged_view(cache, dt, Hq, fp8, &p.c);
   if (rc != SINKATTN_OK) return rc;
   if (Hq / cache->Hkv > kPagedMaxGroup) return SINKATTN_ERR_UNSUPPORTED;
+  if (!fits_int((long long)cache->B * Hq)) return SINKATTN_ERR_INVALID_ARG;
   if (workspace_bytes < sinkattn_paged_decode_workspace_bytes(cache->B, Hq, cache->Hkv, cache->D))
     return SINKATTN_ERR_WORKSPACE;
   p.dt = dt;

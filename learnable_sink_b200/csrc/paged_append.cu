@@ -115,25 +115,37 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     E::pack(x[6], x[7]));
 }
 
+// x c - y s and x c + y s.  EXACT adds the products' own rounding errors back (a
+// fused multiply-add gives them), which leaves half a unit in the last place or
+// little more whatever cancels: an 8-bit code next to a tie then falls as the exact
+// value does.  16-bit results do not show the difference.
+template <bool EXACT>
+__device__ __forceinline__ float turn(float x, float c, float y, float s) {
+  if constexpr (!EXACT) return x * c + y * s;
+  const float w = y * s, e = fmaf(y, s, -w);
+  return fmaf(x, c, w) + e;
+}
+template <bool EXACT>
 __device__ __forceinline__ void rotate_pairs(float (&x)[8], const float* c, const float* s) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float x0 = x[2 * i], x1 = x[2 * i + 1];
-    x[2 * i] = x0 * c[i] - x1 * s[i];
-    x[2 * i + 1] = x1 * c[i] + x0 * s[i];
+    x[2 * i] = turn<EXACT>(x0, c[i], -x1, s[i]);
+    x[2 * i + 1] = turn<EXACT>(x1, c[i], x0, s[i]);
   }
 }
+template <bool EXACT>
 __device__ __forceinline__ void rotate16(float (&a)[8], float (&b)[8], const Angles& t,
                                          const Chunks& ch, int interleaved) {
   if (interleaved) {
-    if (ch.rot_a) rotate_pairs(a, t.c, t.s);
-    if (ch.rot_b) rotate_pairs(b, t.c + 4, t.s + 4);
+    if (ch.rot_a) rotate_pairs<EXACT>(a, t.c, t.s);
+    if (ch.rot_b) rotate_pairs<EXACT>(b, t.c + 4, t.s + 4);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float x = a[i], y = b[i];
-      a[i] = x * t.c[i] - y * t.s[i];
-      b[i] = y * t.c[i] + x * t.s[i];
+      a[i] = turn<EXACT>(x, t.c[i], -y, t.s[i]);
+      b[i] = turn<EXACT>(y, t.c[i], x, t.s[i]);
     }
   }
 }
@@ -217,7 +229,7 @@ __device__ __forceinline__ void token_rows(const PagedAppendProblem& p, int t, i
         float a[8], b[8];
         widen8<E>(xa[u], a);
         widen8<E>(xb[u], b);
-        rotate16(a, b, an, ch, p.interleaved);
+        rotate16<false>(a, b, an, ch, p.interleaved);
         xa[u] = pack8<E>(a);
         xb[u] = pack8<E>(b);
       }
@@ -383,7 +395,7 @@ __global__ void __launch_bounds__(1024) paged_append_fp8_kernel(PagedAppendProbl
     if (on && ch.rot_a) {
       Angles an;
       load_angles(an, p.rope, pos0 + r, p.rot, ch, p.interleaved);
-      rotate16(xa[u], xb[u], an, ch, p.interleaved);
+      rotate16<true>(xa[u], xb[u], an, ch, p.interleaved);
     }
     if (on && !is_v && p.k_out) {
       T* ko = static_cast<T*>(p.k_out) + (t * c.Hkv + h) * D;

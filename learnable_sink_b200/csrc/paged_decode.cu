@@ -35,6 +35,8 @@
 // pair + CTA, which no two segments share, and a second kernel joins them.
 #include <cuda_fp8.h>
 
+#include <climits>
+
 #include "internal.h"
 #include "paged.cuh"
 
@@ -82,9 +84,9 @@ template <int TP>
 struct Walk {
   int b, kvh, t0, cnt;  // the segment: tiles [t0, t0 + cnt) of (b, kvh)
   SeqTiles seq;
-  long long left;       // units of the run from the segment on
+  int left;             // units of the run from the segment on
   __device__ __forceinline__ void cut() {
-    cnt = (int)min((long long)(seq.count - t0), left);
+    cnt = min(seq.count - t0, left);
   }
   // a run that begins behind a pair's tiles begins with the next pair
   __device__ __forceinline__ bool begin(const PagedDecodeProblem& p) {
@@ -102,69 +104,71 @@ struct Walk {
     return true;
   }
 };
-// a / b, with the 32-bit division where it will do (the 64-bit one is a long
-// subroutine, and every CTA's start waits for it)
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
-}
-// CTA i takes units [run_begin(i), run_begin(i + 1)) of the total; with fewer units
+// CTA i of n takes per units, the first `more` of them one more; with fewer units
 // than CTAs the first ones take one each, so that a pair's CTAs are consecutive.
-__device__ __forceinline__ long long run_begin(long long total, int i) {
-  const int n = (int)min((long long)gridDim.x, total);
-  return quotient(total * min(i, n), n);
-}
-__device__ __forceinline__ int cta_of(long long total, long long unit) {
-  const int n = (int)min((long long)gridDim.x, total);
-  return (int)quotient((unit + 1) * n - 1, total);
-}
+// (Units are counted in 32 bits, which the host has checked: a 64-bit division is a
+// long subroutine, and every CTA's start waits for it.)
+struct Runs {
+  int total, per, more;
+  __device__ __forceinline__ explicit Runs(int t) : total(t) {
+    per = t / (int)gridDim.x;
+    more = t - per * (int)gridDim.x;
+  }
+  __device__ __forceinline__ int begin(int i) const { return i * per + min(i, more); }
+  __device__ __forceinline__ int cta_of(int unit) const {
+    const int fat = more * (per + 1);
+    return unit < fat ? unit / (per + 1) : more + (unit - fat) / per;
+  }
+};
 
 template <int TP>
 struct Start {
   Walk<TP> walk;
-  long long first, total;  // the run's first unit; units of all
+  int first, total;  // the run's first unit; units of all
 };
 
 // Adds up the lengths (a slice of the sequences a thread) and finds where this
 // CTA's run begins; the thread whose slice it is in sets the walk up for all.
 template <int THREADS, int TP>
-__device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start<TP>* st,
-                                           long long* s_warp) {
+__device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start<TP>* st, int* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per_thread = (p.c.B + THREADS - 1) / THREADS;
   const int b0 = tid * per_thread, b1 = min(b0 + per_thread, p.c.B);
-  long long sum = 0;
+  int sum = 0;
   for (int b = b0; b < b1; ++b) sum += seq_tiles<TP>(p, b).count + kPairUnits;
-  long long inc = sum;
+  int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
   if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
-  long long before = inc - sum, total = 0;
+  int before = inc - sum, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
+    const int v = s_warp[w];
+    if (w < warp) before += v;
+    total += v;
   }
   total *= p.c.Hkv;
   before *= p.c.Hkv;
-  const long long f0 = run_begin(total, blockIdx.x);
+  const Runs runs(total);
+  const int f0 = runs.begin(blockIdx.x);
   if (f0 >= before && f0 < before + sum * p.c.Hkv) {
     Walk<TP> w;
     w.b = b0;
     for (;;) {
       w.seq = seq_tiles<TP>(p, w.b);
-      const long long units = (long long)(w.seq.count + kPairUnits) * p.c.Hkv;
+      const int units = (w.seq.count + kPairUnits) * p.c.Hkv;
       if (f0 < before + units) break;
       before += units;
       ++w.b;
     }
-    const int rem = (int)(f0 - before), units = w.seq.count + kPairUnits;
+    const int rem = f0 - before, units = w.seq.count + kPairUnits;
     w.kvh = rem / units;
     w.t0 = rem - w.kvh * units;
-    w.left = run_begin(total, blockIdx.x + 1) - f0;
+    w.left = runs.begin(blockIdx.x + 1) - f0;
     w.cut();
     st->walk = w;
     st->first = f0;
@@ -352,7 +356,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   __shared__ int abort_s;
   __shared__ uint32_t tmem_s;
   __shared__ Start<TP> start_s;
-  __shared__ long long warp_s[G_::WARPS];
+  __shared__ int warp_s[G_::WARPS];
   __shared__ __align__(16) float qs_s[8][GP];  // query scales of the last eight segments
   __shared__ float sink_sm[8][GP];             // their sink logits, log2 units
   // (A segment's entries are read up to its result.  The queries of segment s + 8
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   const uint32_t tm_s = tmem, tm_o = tmem + 2 * NT;
 
   Walk<TP> w = start_s.walk;
-  const long long total = start_s.total, f0 = start_s.first, run = w.left;
+  const int total = start_s.total, f0 = start_s.first, run = w.left;
   const bool work = w.begin(p);
 
   if (!work) {
@@ -637,9 +641,9 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       if (w.t0 == 0 && lane == 0) {
         // where the join finds the pair's segments
         const long long pair = (long long)w.b * c.Hkv + w.kvh;
-        const long long first = f0 + run - w.left;
+        const int first = f0 + run - w.left;
         reinterpret_cast<int2*>(p.part)[pair] = make_int2(
-            blockIdx.x, cta_of(total, first + w.seq.count - 1) - (int)blockIdx.x + 1);
+            blockIdx.x, Runs(total).cta_of(first + w.seq.count - 1) - (int)blockIdx.x + 1);
         if (__ldg(c.seqlens + w.b) > w.seq.n) set_status(c.status, SINKATTN_ERR_BOUNDS);
       }
       for (int i = 0; i < w.cnt; ++i, ++j) {
@@ -991,6 +995,7 @@ int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
   // no more CTAs than the tables have tiles
   const long long tiles = ((long long)c.max_pages * c.page_size + G_::TP - 1) / G_::TP;
   long long grid = tiles * c.B * c.Hkv;
+  if ((tiles + kPairUnits) * c.B * c.Hkv > INT_MAX) return SINKATTN_ERR_UNSUPPORTED;
   if (grid > G_::CTAS * sms) grid = G_::CTAS * sms;
   if (grid > kMaxCtas) grid = kMaxCtas;
   record_start(SINKATTN_KERNEL_DECODE, stream);

@@ -578,6 +578,8 @@ def _handle(stream, dev):
     return _raw_stream(dev)
 
 
+_CODE = {torch.bfloat16: BF16, torch.float16: FP16}
+
 # The paged calls serve single tokens, where the host's time counts: their checks
 # are plain comparisons, and what was wrong is put in words only once one fails.
 
@@ -600,16 +602,18 @@ def _token_stride(fn, name, t, shape, dtype, dev):
     T, H, D = shape
     if t.shape != shape or t.dtype != dtype:
         _shape(fn, name, t, shape, dtype)
+    s0, s1, s2 = t.stride()
+    row = H * D
+    if T <= 1:
+        s0 = row
+    if (s2 == 1 and (s1 == D or H == 1) and s0 >= row and not s0 % 8 and not t.data_ptr() % 16
+            and t.get_device() == dev):
+        return s0
     if t.get_device() != dev:
         raise SinkAttnError(fn, 1, f"{name} is on {t.device}, the cache on cuda:{dev}")
-    s0, s1, s2 = t.stride()
-    if T <= 1:
-        s0 = H * D
     if s2 != 1 or (H != 1 and s1 != D):
         raise SinkAttnError(fn, 1, f"{name}: a token's heads must be contiguous")
-    if s0 < H * D or s0 % 8 or t.data_ptr() % 16:
-        raise SinkAttnError(fn, 1, f"{name}: tokens must be 16-byte aligned and not overlap")
-    return s0
+    raise SinkAttnError(fn, 1, f"{name}: tokens must be 16-byte aligned and not overlap")
 
 
 def _paged_append(fn, call, coded, k, v, cache, cu_new, rope, interleaved, q, q_out, k_out, stream):
@@ -625,38 +629,46 @@ def _paged_append(fn, call, coded, k, v, cache, cu_new, rope, interleaved, q, q_
     ks = _token_stride(fn, "k", k, kv, dt, dev)
     vs = _token_stride(fn, "v", v, kv, dt, dev)
     Hq = qs = rot = n_pos = 0
+    q_ptr = qo_ptr = ko_ptr = cu_ptr = rope_ptr = None
     if q is not None:
         if q.dim() != 3:
             raise SinkAttnError(fn, 1, "q must be [T, Hq, D]")
         Hq = q.shape[1]
-        qs = _token_stride(fn, "q", q, (T, Hq, D), dt, dev)
+        shape = (T, Hq, D)
+        qs = _token_stride(fn, "q", q, shape, dt, dev)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
-        elif not _plain(q_out, (T, Hq, D), dt, dev):
-            _refuse_plain(fn, "q_out", q_out, (T, Hq, D), dt, dev)
+            q_out = torch.empty(shape, dtype=dt, device=q.device)
+        elif (q_out.shape != shape or q_out.dtype != dt or q_out.get_device() != dev
+              or not q_out.is_contiguous()):
+            _refuse_plain(fn, "q_out", q_out, shape, dt, dev)
+        q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise SinkAttnError(fn, 1, "q_out without q")
-    if not _plain(k_out, kv, dt, dev):
-        _refuse_plain(fn, "k_out", k_out, kv, dt, dev)
+    if k_out is not None:
+        if not _plain(k_out, kv, dt, dev):
+            _refuse_plain(fn, "k_out", k_out, kv, dt, dev)
+        ko_ptr = k_out.data_ptr()
     if cu_new is None:
         if T != B:
             raise SinkAttnError(fn, 1, f"{T} tokens for {B} sequences without cu_new")
-    elif not _plain(cu_new, (B + 1,), torch.int32, dev):
-        _refuse_plain(fn, "cu_new", cu_new, (B + 1,), torch.int32, dev)
+    else:
+        if not _plain(cu_new, (B + 1,), torch.int32, dev):
+            _refuse_plain(fn, "cu_new", cu_new, (B + 1,), torch.int32, dev)
+        cu_ptr = cu_new.data_ptr()
     if rope is not None:
-        if rope.dim() != 2 or not _plain(rope, rope.shape, torch.float32, dev):
+        if (rope.dim() != 2 or rope.dtype != torch.float32 or rope.get_device() != dev
+                or not rope.is_contiguous()):
             raise SinkAttnError(fn, 1, "rope must be float32 [n_pos, rot_dim], contiguous, on the "
                                        "cache's device")
         n_pos, rot = rope.shape
         if n_pos < 1 or rot % 16 or not 16 <= rot <= D:
             raise SinkAttnError(fn, 1, f"rot_dim {rot}: a multiple of 16 up to {D}")
-    _current(fn, dev)
-    rc = call(_dt(k), T, Hq, cache._ref, k.data_ptr(), ks, v.data_ptr(), vs,
-              None if q is None else q.data_ptr(), qs,
-              None if cu_new is None else cu_new.data_ptr(),
-              None if rope is None else rope.data_ptr(), rot, n_pos, 1 if interleaved else 0,
-              None if q_out is None else q_out.data_ptr(),
-              None if k_out is None else k_out.data_ptr(), _handle(stream, dev))
+        rope_ptr = rope.data_ptr()
+    if dev != torch.cuda.current_device():
+        _current(fn, dev)
+    rc = call(_CODE.get(dt) if dt in _CODE else _dt(k), T, Hq, cache._ref, k.data_ptr(), ks,
+              v.data_ptr(), vs, q_ptr, qs, cu_ptr, rope_ptr, rot, n_pos, 1 if interleaved else 0,
+              qo_ptr, ko_ptr, _handle(stream, dev))
     if rc:
         raise SinkAttnError(fn, rc)
     return q_out
@@ -708,17 +720,26 @@ def _paged_decode(fn, call, coded, q, cache, sink, n_sink, window, scale, stream
     if workspace is None:
         workspace = torch.empty(max(paged_decode_workspace_bytes(B, Hq, cache.Hkv, D), 16),
                                 dtype=torch.uint8, device=q.device)
-    for name, t, want, kind in (("q", q, shape, dt), ("out", out, shape, dt),
-                                ("lse", lse, (B, Hq), torch.float32),
-                                ("sink_s", sink_s, (B, Hq), torch.float32),
-                                ("learnable_sink", sink, (Hq,), torch.float32),
-                                ("workspace", workspace, workspace.shape, workspace.dtype)):
-        if not _plain(t, want, kind, dev):
-            _refuse_plain(fn, name, t, want, kind, dev)
-    _current(fn, dev)
-    rc = call(_dt(q), Hq, D ** -0.5 if scale is None else scale, q.data_ptr(), cache._ref, n_sink,
-              window, None if sink is None else sink.data_ptr(), out.data_ptr(), lse.data_ptr(),
-              sink_s.data_ptr(), workspace.data_ptr(), workspace.nbytes, _handle(stream, dev))
+    f32, rows = torch.float32, (B, Hq)
+    if not (out.shape == shape and out.dtype == dt and lse.shape == rows and lse.dtype == f32
+            and sink_s.shape == rows and sink_s.dtype == f32
+            and q.get_device() == out.get_device() == lse.get_device() == sink_s.get_device()
+            == workspace.get_device() == dev
+            and q.is_contiguous() and out.is_contiguous() and lse.is_contiguous()
+            and sink_s.is_contiguous() and workspace.is_contiguous()
+            and _plain(sink, (Hq,), f32, dev)):
+        for name, t, want, kind in (("q", q, shape, dt), ("out", out, shape, dt),
+                                    ("lse", lse, rows, f32), ("sink_s", sink_s, rows, f32),
+                                    ("learnable_sink", sink, (Hq,), f32),
+                                    ("workspace", workspace, workspace.shape, workspace.dtype)):
+            if not _plain(t, want, kind, dev):
+                _refuse_plain(fn, name, t, want, kind, dev)
+    if dev != torch.cuda.current_device():
+        _current(fn, dev)
+    rc = call(_CODE.get(dt) if dt in _CODE else _dt(q), Hq, D ** -0.5 if scale is None else scale,
+              q.data_ptr(), cache._ref, n_sink, window, None if sink is None else sink.data_ptr(),
+              out.data_ptr(), lse.data_ptr(), sink_s.data_ptr(), workspace.data_ptr(),
+              workspace.nbytes, _handle(stream, dev))
     if rc:
         raise SinkAttnError(fn, rc)
     return out, lse, sink_s

@@ -276,7 +276,11 @@ def test_decode_shared_prefix_pages(fp8):
     p.q[2] = p.q[0]
     got = p.run()
     p.check(got)
-    assert all(torch.equal(t[0], t[2]) for t in got[1:])
+    # The third sequence equals the first, but its work may be cut elsewhere, which orders
+    # the sums differently: a weight is off by 2^-22 (the exponential) and 2^-21 (its
+    # argument, below 16 in log2 units), a sum of them by some 20 additions' 2^-24 each;
+    # together under 2^-18.  LSE and the gate round once more, below 2^-20.
+    assert all((t[0] - t[2]).abs().max() <= 2.0 ** -17 for t in got[1:])
 
 
 def test_decode_bad_pages_and_lengths_set_the_status():
