@@ -715,16 +715,18 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
 #pragma unroll
           for (int h = 0; h < H; ++h) x[0][h] = __uint_as_float(r[h]) * page.x;
         }
-        bool moves = i == 0;
 #pragma unroll
         for (int q = 0; q < PP; ++q) {
           seen[q] = held && visible(p, w.seq.n, pos0 + q);
 #pragma unroll
-          for (int h = 0; h < H; ++h) {
-            x[q][h] = seen[q] ? x[q][h] : -INFINITY;
-            moves |= x[q][h] - ref[0][h] > kLag;
-            if constexpr (F8) moves |= x[q][h] + (lvs - ref[1][h]) > kLag;
-          }
+          for (int h = 0; h < H; ++h) x[q][h] = seen[q] ? x[q][h] : -INFINITY;
+        }
+        bool moves = i == 0;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const float xm = PP == 2 ? fmaxf(x[0][h], x[PP - 1][h]) : x[0][h];
+          moves |= xm - ref[0][h] > kLag;
+          if constexpr (F8) moves |= xm + (lvs - ref[1][h]) > kLag;
         }
         if (any_of_128(moves, wg)) {
           // rare: raise the references to the maxima so far, and bring l and O along
@@ -787,7 +789,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
 #pragma unroll
               for (int t = 0; t < G_::PT; ++t) {
                 const uint32_t two = e4m3x2_of_f16x2(v);
-                pk[t] |= two << (8 * h);
+                pk[t] = h == 0 ? two : __byte_perm(pk[t], two, 0x5410);
                 if (t + 1 < G_::PT)
                   v = __hmul2(__hsub2(v, f16x2_of_e4m3x2(two)), __float2half2_rn(G_::TERM));
               }
