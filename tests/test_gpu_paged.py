@@ -371,6 +371,61 @@ def test_decode_on_two_streams_at_once(fp8):
         p.check(runs[0])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_two_graphs_share_a_workspace(fp8):
+    """Two captured calls of different shapes, replayed in turn over one workspace, and
+    a call on a stream passed by argument."""
+    ps = [Problem([2000, 9, 600], 8, 2, 128, 64, BF, fp8, seed=27), Problem([50, 1300], 16, 2, 128, 64, BF, fp8, seed=28)]
+    ws = torch.empty(max(S.paged_decode_workspace_bytes(3, 8, 2, 128),
+                         S.paged_decode_workspace_bytes(2, 16, 2, 128)), dtype=torch.uint8, device="cuda")
+    call = S.paged_decode_fp8 if fp8 else S.paged_decode
+    graphs, outs, held = [], [], []
+    for p in ps:
+        q, c, sink = p.q.cuda(), p.cache(), p.sink.cuda()
+        held.append((q, c, sink))
+        call(q, c, sink, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(q, c, sink, workspace=ws))
+        graphs.append(g)
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for p, o in zip(ps, outs):
+        p.check(o)
+    side = torch.cuda.Stream()
+    ps[0].check(ps[0].run(stream=side))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_back_to_back_without_a_wait(fp8):
+    """Many calls in a row whose inputs the stream itself changes in between: each
+    starts under the end of the one before it, and none may read too early."""
+    p = Problem([700, 1, 129, 40], 8, 2, 64, 16, BF, fp8, seed=29)
+    c, sink = p.cache(), p.sink.cuda()
+    qs = [torch.randn(p.q.shape, generator=gen(100 + i)).to(BF) for i in range(12)]
+    lens = [torch.tensor([700 - 31 * i, i, 129 - 7 * i, 40 + i], dtype=torch.int32) for i in range(12)]
+    qd, ld = [x.cuda() for x in qs], [x.cuda() for x in lens]
+    q = torch.empty_like(qd[0])
+    call = S.paged_decode_fp8 if fp8 else S.paged_decode
+    ws = torch.empty(S.paged_decode_workspace_bytes(4, 8, 2, 64), dtype=torch.uint8, device="cuda")
+    got = []
+    torch.cuda.synchronize()
+    for i in range(12):
+        q.copy_(qd[i])
+        c.cache_seqlens.copy_(ld[i])
+        got.append(call(q, c, sink, workspace=ws))
+        got.append(call(q, c, sink, workspace=ws))  # the call before it is the same kernel
+    torch.cuda.synchronize()
+    for i in range(12):
+        p.q, p.lens = qs[i], lens[i]
+        want = p.want()
+        p.check(got[2 * i], want)
+        p.check(got[2 * i + 1], want)
+
+
 def test_decode_row_offsets_past_32_bits():
     """Pages whose element offsets pass 2^31."""
     page, D, Hkv = 128, 128, 1
