@@ -49,4 +49,48 @@ size_t paged_decode_part_floats(int B, int Hq, int Hkv, int D, int sms);
 
 constexpr int kPagedMaxGroup = 16;  // query heads per KV head
 
+// ---- the decode's schedule (host and device) --------------------------------
+constexpr int kMaxCtas = 320;
+
+// The tiles (of tp positions) of a sequence of length n that hold visible
+// positions: [0, ts), then f, f + 1, ...; never none, so that a sequence without a
+// key still has a (masked) tile, which writes its result.
+struct SeqTiles {
+  int n, ts, f, count;
+  SeqTiles() = default;
+  __host__ __device__ SeqTiles(int len, int cap, int n_sink, int window, int tp) {
+    n = len < 0 ? 0 : len > cap ? cap : len;
+    const int all = n / tp + (n % tp != 0);
+    ts = all > 1 ? all : 1;
+    f = 0;
+    count = ts;
+    const int w0 = n - window;  // first position of the window
+    if (window > 0 && w0 > n_sink) {
+      ts = n_sink / tp + (n_sink % tp != 0);
+      f = w0 / tp > ts ? w0 / tp : ts;
+      count = ts + all - f;
+    }
+  }
+  __host__ __device__ int tile(int i) const { return i < ts ? i : f + i - ts; }
+};
+
+// A (sequence, KV head) pair is worth its tiles and kPairUnits more, for what its
+// ends cost (queries, first references, result) whatever its length: with 1 a
+// StreamingLLM band over unequal lengths takes 25 us, with 0 30; 2 gives nothing.
+constexpr int kPairUnits = 1;
+
+// CTA i of n takes `per` units, the first `more` CTAs one more; with fewer units
+// than CTAs the first ones take one each, so that a pair's CTAs are consecutive.
+// (Units are counted in 32 bits, which the host has checked: a 64-bit division is a
+// long subroutine, and every CTA's start waits for it.)
+struct Runs {
+  int per, more;
+  __host__ __device__ Runs(int total, int n) : per(total / n), more(total % n) {}
+  __host__ __device__ int begin(int i) const { return i * per + (i < more ? i : more); }
+  __host__ __device__ int cta_of(int unit) const {
+    const int fat = more * (per + 1);
+    return unit < fat ? unit / (per + 1) : more + (unit - fat) / per;
+  }
+};
+
 }  // namespace sk

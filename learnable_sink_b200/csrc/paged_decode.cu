@@ -46,38 +46,15 @@ namespace {
 
 constexpr int kRows = 128;     // rows of a K or V tile
 constexpr int kHeads = 4;      // query heads per softmax warpgroup
-constexpr int kMaxCtas = 320;
 
 // ------------------------------------------------------------------ schedule
-// The tiles of a sequence that hold visible positions: [0, ts), then f, f + 1, ...
-struct SeqTiles {
-  int n, ts, f, count;
-  __device__ __forceinline__ int tile(int i) const { return i < ts ? i : f + i - ts; }
-};
 template <int TP>  // positions per tile
 __device__ __forceinline__ SeqTiles seq_tiles(const PagedDecodeProblem& p, int b) {
-  SeqTiles s;
-  const int cap = p.c.max_pages << p.c.page_log2;
-  s.n = min(max(__ldg(p.c.seqlens + b), 0), cap);
-  const int all = s.n / TP + (s.n % TP != 0);
-  s.ts = max(all, 1);  // a pair without a key still has a (masked) tile, which writes its result
-  s.f = 0;
-  s.count = s.ts;
-  const int w0 = s.n - p.window;
-  if (p.window > 0 && w0 > p.n_sink) {
-    s.ts = p.n_sink / TP + (p.n_sink % TP != 0);
-    s.f = max(w0 / TP, s.ts);
-    s.count = s.ts + all - s.f;
-  }
-  return s;
+  return SeqTiles(__ldg(p.c.seqlens + b), p.c.max_pages << p.c.page_log2, p.n_sink, p.window, TP);
 }
 __device__ __forceinline__ bool visible(const PagedDecodeProblem& p, int n, int pos) {
   return pos < n && (p.window <= 0 || pos < p.n_sink || pos >= n - p.window);
 }
-
-// A pair is worth its tiles and kPairUnits more, for what its ends cost (queries,
-// first references, result) whatever its length.
-constexpr int kPairUnits = 1;
 
 // A CTA's run of units, walked segment by segment (every role walks for itself).
 template <int TP>
@@ -104,23 +81,6 @@ struct Walk {
     return true;
   }
 };
-// CTA i of n takes per units, the first `more` of them one more; with fewer units
-// than CTAs the first ones take one each, so that a pair's CTAs are consecutive.
-// (Units are counted in 32 bits, which the host has checked: a 64-bit division is a
-// long subroutine, and every CTA's start waits for it.)
-struct Runs {
-  int total, per, more;
-  __device__ __forceinline__ explicit Runs(int t) : total(t) {
-    per = t / (int)gridDim.x;
-    more = t - per * (int)gridDim.x;
-  }
-  __device__ __forceinline__ int begin(int i) const { return i * per + min(i, more); }
-  __device__ __forceinline__ int cta_of(int unit) const {
-    const int fat = more * (per + 1);
-    return unit < fat ? unit / (per + 1) : more + (unit - fat) / per;
-  }
-};
-
 template <int TP>
 struct Start {
   Walk<TP> walk;
@@ -153,7 +113,7 @@ __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start<TP
   }
   total *= p.c.Hkv;
   before *= p.c.Hkv;
-  const Runs runs(total);
+  const Runs runs(total, gridDim.x);
   const int f0 = runs.begin(blockIdx.x);
   if (f0 >= before && f0 < before + sum * p.c.Hkv) {
     Walk<TP> w;
@@ -184,11 +144,12 @@ template <class E, int D, bool F8, int NWG>
 struct Geo {
   static constexpr int EB = F8 ? 1 : 2;
   static constexpr int CB = D * EB;                    // bytes of a position
-  // Positions per row of a tile: a copy takes about 4.5 cycles for a row of up to
-  // 128 bytes, so two positions of 64 bytes, neighbours in memory, share one; K's
-  // halves are then multiplied apart, into columns of their own, and V's half rows
-  // with the probabilities of their own positions (a StreamingLLM band, with
-  // the leaner softmax that it made room for: 24.7 -> 23.1 us).
+  // Positions per row of a tile.  A warp spends about 85 cycles on a copy of 1 KB and
+  // 125 on one of 4 KB, and a tile has its barriers and votes whatever it holds; so two
+  // positions of 64 bytes, neighbours in memory, share a row: K's halves are multiplied
+  // apart, into columns of their own, and V's half rows with the probabilities of their
+  // own positions (a StreamingLLM band, with the leaner softmax that it made room for:
+  // 24.7 -> 23.1 us).
   static constexpr int PP = CB == 64 ? 2 : 1;
   static constexpr int TP = kRows * PP;                // positions per tile
   static constexpr int RB = CB * PP;                   // bytes of a row
@@ -231,7 +192,8 @@ struct Geo {
 // most 2^kLag they stay within 2^8 (E4M3 reaches 448), as high as they can.  The
 // 8-bit terms are split in f16 pairs: its eleven bits are what three terms hold, a
 // residue and its move by 2^5 are exact in it, and it takes half the instructions
-// of float32 (its last bit, 2^-24, lies below the third term's, 2^-20).
+// of float32 (its last bit, 2^-24, lies below the third term's, 2^-20).  Where the
+// result is f16 too, what the first rounding to f16 left goes into the third term.
 constexpr float kLag = 2.f, kBase = 6.f;
 
 template <bool F8>
@@ -644,7 +606,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
         const long long pair = (long long)w.b * c.Hkv + w.kvh;
         const int first = f0 + run - w.left;
         reinterpret_cast<int2*>(p.part)[pair] = make_int2(
-            blockIdx.x, Runs(total).cta_of(first + w.seq.count - 1) - (int)blockIdx.x + 1);
+            blockIdx.x, Runs(total, gridDim.x).cta_of(first + w.seq.count - 1) - (int)blockIdx.x + 1);
         if (__ldg(c.seqlens + w.b) > w.seq.n) set_status(c.status, SINKATTN_ERR_BOUNDS);
       }
       for (int i = 0; i < w.cnt; ++i, ++j) {
@@ -786,9 +748,15 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
               e[k] = F8 ? fast_exp2(x[q][h + k] + (lvs - ref[1][h + k] + kBase)) : pr * 64.f;
             }
             if constexpr (F8) {
-              __half2 v = __floats2half2_rn(e[0], e[1]);
+              __half2 v = __floats2half2_rn(e[0], e[1]), rest{};
+              if constexpr (E::kFmt == 0) {
+                const float2 f = __half22float2(v);
+                rest = __floats2half2_rn((e[0] - f.x) * (G_::TERM * G_::TERM),
+                                         (e[1] - f.y) * (G_::TERM * G_::TERM));
+              }
 #pragma unroll
               for (int t = 0; t < G_::PT; ++t) {
+                if (E::kFmt == 0 && t == G_::PT - 1) v = __hadd2(v, rest);
                 const uint32_t two = e4m3x2_of_f16x2(v);
                 pk[t] = h == 0 ? two : __byte_perm(pk[t], two, 0x5410);
                 if (t + 1 < G_::PT)

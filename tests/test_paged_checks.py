@@ -2,6 +2,8 @@
 metadata checks (CPU tensors; a valid call stops at the device check), and pins
 of the float64 oracle that the GPU tests compare with."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -10,6 +12,7 @@ import torch
 import oracle
 from learnable_sink_b200 import sinkattn as S
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 bf, f16, f32, i32 = torch.bfloat16, torch.float16, torch.float32, torch.int32
 B, Hq, Hkv, D, PAGE, NP, MP = 3, 8, 2, 64, 16, 12, 4
 
@@ -99,6 +102,17 @@ def test_workspace_query():
     assert f(0, 8, 2, 64) == 0 and f(1, 7, 2, 64) == 0 and f(1, 8, 2, 96) == 0
     # a partial of every query head for each sequence and KV head at least
     assert f(32, 32, 8, 128) >= 32 * 32 * 130 * 4
+
+
+def test_decode_schedule_covers_every_position_once(tmp_path):
+    """The paged decode's schedule (host code, compiled and run on the CPU): every
+    visible position in one tile, partial slots distinct and inside the workspace."""
+    from learnable_sink_b200 import build
+    exe = str(tmp_path / "paged_schedule_check")
+    subprocess.check_call([build.nvcc(), "-std=c++17", "-arch=sm_100a", "-I", os.path.join(ROOT, "include"),
+                           os.path.join(ROOT, "tests", "c", "paged_schedule_check.cu"), "-o", exe])
+    out = subprocess.run([exe], capture_output=True, text=True)
+    assert out.returncode == 0 and out.stdout.startswith("ok "), out.stdout
 
 
 # ------------------------------------------------------------------ binding
