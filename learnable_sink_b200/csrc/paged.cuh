@@ -52,26 +52,32 @@ constexpr int kPagedMaxGroup = 16;  // query heads per KV head
 // ---- the decode's schedule (host and device) --------------------------------
 constexpr int kMaxCtas = 320;
 
-// The tiles (of tp positions) of a sequence of length n that hold visible
-// positions: [0, ts), then f, f + 1, ...; never none, so that a sequence without a
-// key still has a (masked) tile, which writes its result.
+// The pages of a sequence that hold visible positions, [0, sp) for the sink tokens
+// and then fp, fp + 1, ..., cut into tiles of tp positions: a window's tiles begin at
+// its own first page, behind the sink tokens' (so four sink tokens cost a page of a
+// tile, not a tile).  There is always a tile, which writes the result of a sequence
+// without a key.
 struct SeqTiles {
-  int n, ts, f, count;
+  int n, sp, fp, pages, count;
   SeqTiles() = default;
-  __host__ __device__ SeqTiles(int len, int cap, int n_sink, int window, int tp) {
+  __host__ __device__ SeqTiles(int len, int cap, int n_sink, int window, int page_log2, int tp) {
+    const int size = 1 << page_log2;
     n = len < 0 ? 0 : len > cap ? cap : len;
-    const int all = n / tp + (n % tp != 0);
-    ts = all > 1 ? all : 1;
-    f = 0;
-    count = ts;
+    pages = n / size + (n % size != 0);
+    sp = pages;
+    fp = 0;
     const int w0 = n - window;  // first position of the window
     if (window > 0 && w0 > n_sink) {
-      ts = n_sink / tp + (n_sink % tp != 0);
-      f = w0 / tp > ts ? w0 / tp : ts;
-      count = ts + all - f;
+      sp = n_sink / size + (n_sink % size != 0);
+      fp = w0 / size > sp ? w0 / size : sp;
+      pages = sp + pages - fp;
     }
+    const int ppt = tp >> page_log2;
+    count = pages / ppt + (pages % ppt != 0);
+    if (count < 1) count = 1;
   }
-  __host__ __device__ int tile(int i) const { return i < ts ? i : f + i - ts; }
+  // the i-th of the pages
+  __host__ __device__ int page(int i) const { return i < sp ? i : fp + i - sp; }
 };
 
 // A (sequence, KV head) pair is worth its tiles and kPairUnits more, for what its

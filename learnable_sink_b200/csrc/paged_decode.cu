@@ -50,7 +50,8 @@ constexpr int kHeads = 4;      // query heads per softmax warpgroup
 // ------------------------------------------------------------------ schedule
 template <int TP>  // positions per tile
 __device__ __forceinline__ SeqTiles seq_tiles(const PagedDecodeProblem& p, int b) {
-  return SeqTiles(__ldg(p.c.seqlens + b), p.c.max_pages << p.c.page_log2, p.n_sink, p.window, TP);
+  return SeqTiles(__ldg(p.c.seqlens + b), p.c.max_pages << p.c.page_log2, p.n_sink, p.window,
+                  p.c.page_log2, TP);
 }
 __device__ __forceinline__ bool visible(const PagedDecodeProblem& p, int n, int pos) {
   return pos < n && (p.window <= 0 || pos < p.n_sink || pos >= n - p.window);
@@ -386,16 +387,11 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
     bool ok = true;
     do {
       auto load_id = [&](int i) {  // lane's page of tile i, -1: none to bring
+        const int k = (w.t0 + i) * ppt + lane;
         int id = -1;
-        if (lane < ppt && i < w.cnt) {
-          const int page = w.seq.tile(w.t0 + i) * ppt + lane;
-          const int pos = page << c.page_log2;
-          if (pos < w.seq.n && (p.window <= 0 || pos < p.n_sink ||
-                                pos + c.page_size > w.seq.n - p.window))
-            id = __ldg(c.table + (long long)w.b * c.max_pages + page);
-          if (id >= c.n_pages) id = -1;
-        }
-        return id;
+        if (lane < ppt && i < w.cnt && k < w.seq.pages)
+          id = __ldg(c.table + (long long)w.b * c.max_pages + w.seq.page(k));
+        return id < c.n_pages ? id : -1;
       };
       int next = load_id(0);
       for (int i = 0; i < w.cnt && ok; ++i) {
@@ -585,17 +581,13 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
     bool ok = true;
     do {
       auto load_id = [&](int i) {
-        int id = -2;  // no visible position
-        if (lane < ppt && i < w.cnt) {
-          const int page = w.seq.tile(w.t0 + i) * ppt + lane;
-          const int pos = page << c.page_log2;
-          if (pos < w.seq.n && (p.window <= 0 || pos < p.n_sink ||
-                                pos + c.page_size > w.seq.n - p.window)) {
-            id = __ldg(c.table + (long long)w.b * c.max_pages + page);
-            if (id < 0 || id >= c.n_pages) {
-              set_status(c.status, SINKATTN_ERR_BOUNDS);
-              id = -1;
-            }
+        const int k = (w.t0 + i) * ppt + lane;
+        int id = -2;  // no page here
+        if (lane < ppt && i < w.cnt && k < w.seq.pages) {
+          id = __ldg(c.table + (long long)w.b * c.max_pages + w.seq.page(k));
+          if (id < 0 || id >= c.n_pages) {
+            set_status(c.status, SINKATTN_ERR_BOUNDS);
+            id = -1;
           }
         }
         return id;
@@ -636,6 +628,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
     float(&ref)[2][H] = ref_s[wg];
     float(&corr)[2][H] = corr_s[wg];
     float(&red)[4][2 * H] = red_s[wg];
+    const int ppt = TP >> c.page_log2;
     const long long pairs = (long long)c.B * c.Hkv;
     float* parts = p.part + meta_floats(pairs);
     int j = 0, seg = 0;
@@ -647,7 +640,11 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       for (int h = 0; h < H; ++h) l[h] = 0.f;
       if (wt < 2 * H) ref[wt / H][wt % H] = kNone;
       for (int i = 0; i < w.cnt; ++i, ++j) {
-        const int pos0 = w.seq.tile(w.t0 + i) * TP + wt * PP;
+        // the thread's positions (past the last page: past the sequence)
+        const int at_page = (w.t0 + i) * ppt + (wt * PP >> c.page_log2);
+        const int pos0 = at_page < w.seq.pages ? (w.seq.page(at_page) << c.page_log2) +
+                                                     (wt * PP & (c.page_size - 1))
+                                               : w.seq.n;
         mbar_wait(&bar.s_full[j & 1], (j >> 1) & 1, &abort_s, c.status);
         tc_fence_after();
         const float2 page = page_s[j & 1][wt * PP >> c.page_log2];

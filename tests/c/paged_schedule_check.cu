@@ -21,6 +21,7 @@ int main() {
   for (int round = 0; round < 400; ++round) {
     const int B = 1 + std::rand() % (round % 5 == 0 ? 300 : 9), Hkv = 1 + std::rand() % 5;
     const int tp = round % 2 ? 128 : 256, cap = 128 * (1 + std::rand() % 40);
+    const int lg = 4 + std::rand() % 4, ppt = tp >> lg;
     const int n_sink = round % 3 ? 0 : std::rand() % 300, window = round % 4 ? 0 : 1 + std::rand() % 2000;
     std::vector<int> len(B);
     for (int& n : len) n = std::rand() % (cap + 200) - 20;
@@ -29,7 +30,7 @@ int main() {
     std::vector<long long> first(B);
     for (int b = 0; b < B; ++b) {
       first[b] = total;
-      total += (long long)Hkv * (SeqTiles(len[b], cap, n_sink, window, tp).count + kPairUnits);
+      total += (long long)Hkv * (SeqTiles(len[b], cap, n_sink, window, lg, tp).count + kPairUnits);
     }
     const Runs runs((int)total, n_cta);
     if (runs.begin(0) != 0 || runs.begin(n_cta) != total) return std::printf("runs do not cover\n"), 1;
@@ -42,7 +43,7 @@ int main() {
       while (u < end) {
         int b = 0;
         while (b + 1 < B && first[b + 1] <= u) ++b;
-        const SeqTiles s(len[b], cap, n_sink, window, tp);
+        const SeqTiles s(len[b], cap, n_sink, window, lg, tp);
         const int units = s.count + kPairUnits, rem = (int)(u - first[b]);
         const int kvh = rem / units, t0 = rem % units;
         const size_t pair = (size_t)b * Hkv + kvh;
@@ -57,9 +58,12 @@ int main() {
           --left[pair];
           if (pair + c >= slot.size() || slot[pair + c]) return std::printf("partial slot\n"), 1;
           slot[pair + c] = 1;
-          seen[pair].resize((size_t)cap + 2 * tp);
-          for (int i = 0; i < cnt; ++i)
-            for (int k = 0; k < tp; ++k) ++seen[pair][(size_t)s.tile(t0 + i) * tp + k];
+          seen[pair].resize((size_t)cap);
+          for (int k = t0 * ppt; k < (t0 + cnt) * ppt && k < s.pages; ++k) {
+            const long long at = (long long)s.page(k) << lg;
+            if (at < 0 || at + (1 << lg) > cap) return std::printf("page outside the table\n"), 1;
+            for (int i = 0; i < 1 << lg; ++i) ++seen[pair][at + i];
+          }
         }
         u += units - t0;
         if (u > end) u = end;
