@@ -4,7 +4,9 @@
 
 Each .cu under csrc/ is compiled to an object (in parallel) and linked into
 learnable_sink_b200/libsinkattn.so.  Objects are rebuilt when their source
-or any header (csrc/*.cuh, csrc/*.h, include/*.h) is newer.
+or any header (csrc/*.cuh, csrc/*.h, include/*.h) is newer.  The Python side's
+own extension (csrc/binding.cpp: the short way for the paged calls) is compiled
+with g++ against torch's headers into learnable_sink_b200/_binding.so.
 """
 from __future__ import annotations
 
@@ -21,6 +23,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsinkattn.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -55,8 +58,39 @@ def _compile(src: str, force: bool, verbose: bool, extra) -> str:
     return obj
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/binding.cpp; it calls the library by the addresses that the
+    Python side hands it, so it links against torch alone."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and os.path.exists(BINDING) and \
+            os.path.getmtime(BINDING) >= max(os.path.getmtime(src), _newest_header()):
+        return BINDING
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in (os.path.join(home, "include"),
+              os.path.join(home, "include", "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
+        cmd += ["-isystem", d]
+    cmd += [src, "-o", tmp, "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on binding.cpp")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(OBJ, exist_ok=True)
+    build_binding(force, verbose)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(lambda s: _compile(s, force, verbose, extra), srcs))

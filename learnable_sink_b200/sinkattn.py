@@ -117,6 +117,27 @@ def lib():
     return _lib
 
 
+_short = None
+
+
+def _short_way():
+    """The paged calls' short way (csrc/binding.cpp): it checks the tensors and
+    makes the C ABI call in one step, or declines (-1) without a launch."""
+    global _short
+    if _short is None:
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError("learnable_sink_b200/_binding.so is missing or does not load: build it "
+                              "with `python -m learnable_sink_b200.build`") from e
+        L = lib()
+        _binding.bind(*(_c.cast(f, _vp).value for f in (
+            L.sinkattn_paged_append, L.sinkattn_paged_append_fp8,
+            L.sinkattn_paged_decode, L.sinkattn_paged_decode_fp8)))
+        _short = _binding
+    return _short
+
+
 def error_string(code: int) -> str:
     return lib().sinkattn_error_string(code).decode()
 
@@ -512,7 +533,7 @@ class PagedCache:
     are checked once, here, and kept; their contents may change between calls."""
 
     __slots__ = ("k_pages", "v_pages", "block_table", "cache_seqlens", "k_scale", "v_scale",
-                 "device", "B", "Hkv", "D", "_c", "_ref", "_dev")
+                 "device", "B", "Hkv", "D", "_c", "_ref", "_dev", "_at", "_kind")
 
     def __init__(self, k_pages, v_pages, block_table, cache_seqlens, k_scale=None, v_scale=None):
         fn = "PagedCache"
@@ -550,6 +571,8 @@ class PagedCache:
                               block_table.data_ptr(), cache_seqlens.data_ptr(), B, n_pages,
                               page_size, max_pages, Hkv, D)
         self._ref = _c.byref(self._c)
+        self._at = _c.addressof(self._c)
+        self._kind = 2 if coded else int(k_pages.dtype == torch.float16)
 
 
 def _one_device(fn, *ts):
@@ -636,9 +659,7 @@ def _paged_append(fn, call, coded, k, v, cache, cu_new, rope, interleaved, q, q_
         Hq = q.shape[1]
         shape = (T, Hq, D)
         qs = _token_stride(fn, "q", q, shape, dt, dev)
-        if q_out is None:
-            q_out = torch.empty(shape, dtype=dt, device=q.device)
-        elif (q_out.shape != shape or q_out.dtype != dt or q_out.get_device() != dev
+        if (q_out.shape != shape or q_out.dtype != dt or q_out.get_device() != dev
               or not q_out.is_contiguous()):
             _refuse_plain(fn, "q_out", q_out, shape, dt, dev)
         q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
@@ -674,6 +695,24 @@ def _paged_append(fn, call, coded, k, v, cache, cu_new, rope, interleaved, q, q_
     return q_out
 
 
+_APPEND = ("sinkattn_paged_append", "sinkattn_paged_append_fp8")
+_DECODE = ("sinkattn_paged_decode", "sinkattn_paged_decode_fp8")
+
+
+def _append_call(coded, k, v, cache, cu_new, rope, interleaved, q, q_out, k_out, stream):
+    if q_out is None and q is not None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if stream is None:
+        rc = (_short or _short_way()).paged_append(cache._at, coded, cache._kind, cache._dev, k, v,
+                                                   cu_new, rope, interleaved, q, q_out, k_out)
+        if rc == 0:
+            return q_out
+        if rc > 0:
+            raise SinkAttnError(_APPEND[coded], rc)
+    return _paged_append(_APPEND[coded], getattr(lib(), _APPEND[coded]), coded, k, v, cache, cu_new,
+                         rope, interleaved, q, q_out, k_out, stream)
+
+
 def paged_append(k, v, cache: PagedCache, cu_new=None, rope=None, interleaved: bool = False,
                  q=None, q_out=None, k_out=None, stream=None):
     """Append packed new tokens (k/v [T, Hkv, D], sequences by cu_new int32
@@ -683,8 +722,7 @@ def paged_append(k, v, cache: PagedCache, cu_new=None, rope=None, interleaved: b
     interleaved).  ``q`` [T, Hq, D] is rotated into q_out, the rotated keys also
     go to k_out if given.  k, v and q may be views with strided tokens.
     Returns q_out."""
-    return _paged_append("sinkattn_paged_append", lib().sinkattn_paged_append, False, k, v, cache,
-                         cu_new, rope, interleaved, q, q_out, k_out, stream)
+    return _append_call(0, k, v, cache, cu_new, rope, interleaved, q, q_out, k_out, stream)
 
 
 def paged_append_fp8(k, v, cache: PagedCache, cu_new=None, rope=None, interleaved: bool = False,
@@ -692,12 +730,36 @@ def paged_append_fp8(k, v, cache: PagedCache, cu_new=None, rope=None, interleave
     """paged_append into an 8-bit cache: E4M3 codes with a power-of-two scale for
     each page and KV head, which grows (the page's earlier codes with it) when
     new rows need it."""
-    return _paged_append("sinkattn_paged_append_fp8", lib().sinkattn_paged_append_fp8, True, k, v,
-                         cache, cu_new, rope, interleaved, q, q_out, k_out, stream)
+    return _append_call(1, k, v, cache, cu_new, rope, interleaved, q, q_out, k_out, stream)
 
 
 def paged_decode_workspace_bytes(B, Hq, Hkv, D) -> int:
     return int(lib().sinkattn_paged_decode_workspace_bytes(B, Hq, Hkv, D))
+
+
+def _decode_call(coded, q, cache, sink, n_sink, window, scale, stream, workspace, out, lse, sink_s):
+    if out is None or lse is None or sink_s is None or workspace is None:
+        if q.dim() != 3:
+            raise SinkAttnError(_DECODE[coded], 1, "q must be [B, Hq, D]")
+        B, Hq, D = q.shape
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if lse is None:
+            lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+        if sink_s is None:
+            sink_s = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(max(paged_decode_workspace_bytes(B, Hq, cache.Hkv, D), 16),
+                                    dtype=torch.uint8, device=q.device)
+    if stream is None:
+        rc = (_short or _short_way()).paged_decode(cache._at, coded, cache._kind, cache._dev, q, sink,
+                                                   n_sink, window, scale, workspace, out, lse, sink_s)
+        if rc == 0:
+            return out, lse, sink_s
+        if rc > 0:
+            raise SinkAttnError(_DECODE[coded], rc)
+    return _paged_decode(_DECODE[coded], getattr(lib(), _DECODE[coded]), coded, q, cache, sink, n_sink,
+                         window, scale, stream, workspace, out, lse, sink_s)
 
 
 def _paged_decode(fn, call, coded, q, cache, sink, n_sink, window, scale, stream, workspace, out,
@@ -711,15 +773,6 @@ def _paged_decode(fn, call, coded, q, cache, sink, n_sink, window, scale, stream
         _want(fn, cache.k_scale is not None, "the cache is not an 8-bit cache")
     elif cache.k_pages.dtype != dt:
         raise SinkAttnError(fn, 1, f"k_pages is {cache.k_pages.dtype}, expected {dt}")
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    if lse is None:
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
-    if sink_s is None:
-        sink_s = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(max(paged_decode_workspace_bytes(B, Hq, cache.Hkv, D), 16),
-                                dtype=torch.uint8, device=q.device)
     f32, rows = torch.float32, (B, Hq)
     if not (out.shape == shape and out.dtype == dt and lse.shape == rows and lse.dtype == f32
             and sink_s.shape == rows and sink_s.dtype == f32
@@ -736,8 +789,8 @@ def _paged_decode(fn, call, coded, q, cache, sink, n_sink, window, scale, stream
                 _refuse_plain(fn, name, t, want, kind, dev)
     if dev != torch.cuda.current_device():
         _current(fn, dev)
-    rc = call(_CODE.get(dt) if dt in _CODE else _dt(q), Hq, D ** -0.5 if scale is None else scale,
-              q.data_ptr(), cache._ref, n_sink, window, None if sink is None else sink.data_ptr(),
+    rc = call(_CODE.get(dt) if dt in _CODE else _dt(q), Hq, D ** -0.5 if scale is None else float(scale),
+              q.data_ptr(), cache._ref, int(n_sink), int(window), None if sink is None else sink.data_ptr(),
               out.data_ptr(), lse.data_ptr(), sink_s.data_ptr(), workspace.data_ptr(),
               workspace.nbytes, _handle(stream, dev))
     if rc:
@@ -751,16 +804,14 @@ def paged_decode(q, cache: PagedCache, sink, n_sink: int = 0, window: int = 0,
     """One query token per sequence (q [B, Hq, D]) over a paged 16-bit cache;
     with window > 0 only the first n_sink and the last ``window`` positions are
     visible.  Returns (out [B,Hq,D], lse_new [B,Hq], sink_s [B,Hq])."""
-    return _paged_decode("sinkattn_paged_decode", lib().sinkattn_paged_decode, False, q, cache,
-                         sink, n_sink, window, scale, stream, workspace, out, lse, sink_s)
+    return _decode_call(0, q, cache, sink, n_sink, window, scale, stream, workspace, out, lse, sink_s)
 
 
 def paged_decode_fp8(q, cache: PagedCache, sink, n_sink: int = 0, window: int = 0,
                      scale: Optional[float] = None, stream=None, workspace=None, out=None,
                      lse=None, sink_s=None):
     """paged_decode over an 8-bit cache (q and out bfloat16 or float16)."""
-    return _paged_decode("sinkattn_paged_decode_fp8", lib().sinkattn_paged_decode_fp8, True, q,
-                         cache, sink, n_sink, window, scale, stream, workspace, out, lse, sink_s)
+    return _decode_call(1, q, cache, sink, n_sink, window, scale, stream, workspace, out, lse, sink_s)
 
 
 KERNEL_FWD, KERNEL_BWD, KERNEL_DECODE, KERNEL_GATE = 0, 1, 2, 3

@@ -683,6 +683,36 @@ def test_append_out_of_bounds_positions_write_nothing(fp8):
             assert torch.equal(cache.k_pages[at, :, r].cpu(), c["k"][at, :, r])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_the_calls_two_ways_agree(fp8):
+    """A call with a stream argument takes the Python path, one without the short way
+    through the extension; both allocate what is not given, and give the same bits."""
+    Hq, Hkv, D, page = 8, 2, 64, 32
+    c = append_case([1] * 5, [0, 31, 32, 100, 7], Hq, Hkv, D, page, F16, 32, 47, fp8)
+    f = lambda t: None if t is None else t.cuda()  # noqa: E731
+    x = c["x"][:5].cuda()
+    res = []
+    for stream in (None, torch.cuda.current_stream()):
+        cache = S.PagedCache(f(c["k"]), f(c["v"]), f(c["table"]), f(c["lens"]), f(c["ks"]), f(c["vs"]))
+        append = S.paged_append_fp8 if fp8 else S.paged_append
+        attend = S.paged_decode_fp8 if fp8 else S.paged_decode
+        k_out = torch.empty(5, Hkv, D, dtype=F16, device="cuda")
+        q = append(x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], cache, None, c["rope"].cuda(), True, x[:, :Hq],
+                   k_out=k_out, stream=stream)
+        out = attend(q, cache, None, n_sink=2, window=50, stream=stream)
+        torch.cuda.synchronize()
+        res.append([q, k_out, cache.k_pages, cache.v_pages, *out])
+        assert S._short_way().paged_append(cache._at, int(fp8), cache._kind, cache._dev, x[:, :Hkv], x[:, :Hkv],
+                                           None, None, False, x[:, :Hq], None, None) == -1
+        assert S._short_way().paged_decode(cache._at, 1 - int(fp8), cache._kind, cache._dev, q, None, 0, 0,
+                                           None, q, out[0], out[1], out[2]) == -1
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+    with pytest.raises(S.SinkAttnError, match="WORKSPACE"):
+        attend(q, cache, None, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(S.SinkAttnError, match="INVALID_ARG"):
+        attend(q, cache, None, window=-1)
+
+
 def test_append_many_sequences_and_no_token():
     """More sequences than a warp's first search step covers, most without a token;
     T = 0 does nothing."""

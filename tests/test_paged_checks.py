@@ -216,6 +216,23 @@ def test_decode_metadata_mismatches_are_refused(caches):
     _refused(lambda: S.paged_decode(q, c16, sink, workspace=ws, sink_s=torch.zeros(B, 1)), "sink_s")
 
 
+def test_short_way_declines_what_it_does_not_handle(caches):
+    """The extension makes no call for tensors off the GPU, other objects, or values
+    out of range: the Python path then says what is wrong."""
+    c16, _ = caches
+    k = torch.zeros(B, Hkv, D, dtype=bf)
+    a = S._short_way().paged_append
+    head = (c16._at, 0, c16._kind, c16._dev)
+    assert a(*head, k, k, None, None, False, None, None, None) == -1
+    assert a(*head, "k", k, None, None, False, None, None, None) == -1
+    assert a(0, 0, 0, 0, k, k, None, None, False, None, None, None) == -1
+    d = S._short_way().paged_decode
+    q = torch.zeros(B, Hq, D, dtype=bf)
+    assert d(*head, q, None, 0, 0, None, q, q, q, q) == -1
+    with pytest.raises(TypeError):
+        d(1, 2)
+
+
 # ------------------------------------------------------------------ the oracle
 def test_oracle_rotation_closed_forms():
     rope = oracle.rope_table(40, 4, base=100.0)
