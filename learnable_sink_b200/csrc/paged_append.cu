@@ -150,6 +150,14 @@ __device__ __forceinline__ void rotate16(float (&a)[8], float (&b)[8], const Ang
   }
 }
 
+// Both kernels are programmatic dependents (their launch lies under the end of the
+// kernel before them, whose writes the wait makes visible) and let the next one be
+// scheduled at once.
+__device__ __forceinline__ void join_stream() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Where a packed token goes.
 struct Place {
   int b, pos;  // b < 0: no sequence of the call has it, or it is out of bounds
@@ -255,6 +263,7 @@ struct AppendCfg {
 
 template <class E, int D>
 __global__ void __launch_bounds__(kAppendThreads, AppendCfg<D>::BLOCKS) paged_append_kernel(PagedAppendProblem p, int NG) {
+  join_stream();
   constexpr int NC = D / 16;
   const int per_token = NC * NG;  // a multiple of 32: a warp stays in one token
   const long long t =
@@ -316,6 +325,7 @@ __global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendPro
   constexpr int PASSES = kBlockRows / RPP;
   __shared__ float s_max[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  join_stream();
   // page blocks and query blocks alternate, in proportion, so that one kind's
   // waits lie under the other's traffic
   const unsigned before = unsigned((unsigned long long)blockIdx.x * page_blocks / gridDim.x);
@@ -443,6 +453,20 @@ __global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendPro
   if (lane == 0 && row_base == 0) *scale_at = s;
 }
 
+template <class... A>
+int launch_dependent(void (*kern)(A...), unsigned blocks, int threads, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA;
+}
+
 // Row groups of a token's threads: eight leave a thread several rows, whose
 // loads overlap and share its angles; with few tokens the whole block of 256
 // threads takes one token, for latency.
@@ -453,8 +477,7 @@ int append_typed(const PagedAppendProblem& p, cudaStream_t stream) {
   const int NG = row_groups(p.T, D), per_token = D / 16 * NG;
   const long long blocks = ((long long)p.T * per_token + kAppendThreads - 1) / kAppendThreads;
   if (blocks > 0x7fffffffLL) return SINKATTN_ERR_INVALID_ARG;
-  paged_append_kernel<E, D><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p, NG);
-  return cudaGetLastError() == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA;
+  return launch_dependent(paged_append_kernel<E, D>, (unsigned)blocks, kAppendThreads, stream, p, NG);
 }
 
 template <class E, int D>
@@ -466,9 +489,8 @@ int append_fp8_typed(const PagedAppendProblem& p, cudaStream_t stream) {
   const int tokens = threads / (D / 16 * NG);
   const long long q_blocks = p.q ? (p.T + tokens - 1) / tokens : 0;
   if (pages + q_blocks > 0x7fffffffLL) return SINKATTN_ERR_INVALID_ARG;
-  paged_append_fp8_kernel<E, D><<<(unsigned)(pages + q_blocks), threads, 0, stream>>>(
-      p, (int)items, (unsigned)pages, NG);
-  return cudaGetLastError() == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA;
+  return launch_dependent(paged_append_fp8_kernel<E, D>, (unsigned)(pages + q_blocks), threads, stream,
+                          p, (int)items, (unsigned)pages, NG);
 }
 
 }  // namespace
