@@ -53,27 +53,28 @@ constexpr int kPagedMaxGroup = 16;  // query heads per KV head
 constexpr int kMaxCtas = 320;
 
 // The pages of a sequence that hold visible positions, [0, sp) for the sink tokens
-// and then fp, fp + 1, ..., cut into tiles of tp positions: a window's tiles begin at
+// and then fp, fp + 1, ..., cut into tiles of so many pages: a window's tiles begin at
 // its own first page, behind the sink tokens' (so four sink tokens cost a page of a
 // tile, not a tile).  There is always a tile, which writes the result of a sequence
 // without a key.
 struct SeqTiles {
   int n, sp, fp, pages, count;
   SeqTiles() = default;
-  __host__ __device__ SeqTiles(int len, int cap, int n_sink, int window, int page_log2, int tp) {
-    const int size = 1 << page_log2;
+  // ppt_log2: pages per tile (shifts: every CTA's start waits for this)
+  __host__ __device__ SeqTiles(int len, int cap, int n_sink, int window, int page_log2,
+                               int ppt_log2) {
     n = len < 0 ? 0 : len > cap ? cap : len;
-    pages = n / size + (n % size != 0);
+    const int rest = (1 << page_log2) - 1;
+    pages = (n >> page_log2) + ((n & rest) != 0);
     sp = pages;
     fp = 0;
     const int w0 = n - window;  // first position of the window
     if (window > 0 && w0 > n_sink) {
-      sp = n_sink / size + (n_sink % size != 0);
-      fp = w0 / size > sp ? w0 / size : sp;
+      sp = (n_sink >> page_log2) + ((n_sink & rest) != 0);
+      fp = w0 >> page_log2 > sp ? w0 >> page_log2 : sp;
       pages = sp + pages - fp;
     }
-    const int ppt = tp >> page_log2;
-    count = pages / ppt + (pages % ppt != 0);
+    count = (pages >> ppt_log2) + ((pages & ((1 << ppt_log2) - 1)) != 0);
     if (count < 1) count = 1;
   }
   // the i-th of the pages

@@ -48,10 +48,10 @@ constexpr int kRows = 128;     // rows of a K or V tile
 constexpr int kHeads = 4;      // query heads per softmax warpgroup
 
 // ------------------------------------------------------------------ schedule
-template <int TP>  // positions per tile
+template <int TP>  // positions per tile, 128 or 256
 __device__ __forceinline__ SeqTiles seq_tiles(const PagedDecodeProblem& p, int b) {
   return SeqTiles(__ldg(p.c.seqlens + b), p.c.max_pages << p.c.page_log2, p.n_sink, p.window,
-                  p.c.page_log2, TP);
+                  p.c.page_log2, (TP == 128 ? 7 : 8) - p.c.page_log2);
 }
 __device__ __forceinline__ bool visible(const PagedDecodeProblem& p, int n, int pos) {
   return pos < n && (p.window <= 0 || pos < p.n_sink || pos >= n - p.window);

@@ -21,7 +21,7 @@ int main() {
   for (int round = 0; round < 400; ++round) {
     const int B = 1 + std::rand() % (round % 5 == 0 ? 300 : 9), Hkv = 1 + std::rand() % 5;
     const int tp = round % 2 ? 128 : 256, cap = 128 * (1 + std::rand() % 40);
-    const int lg = 4 + std::rand() % 4, ppt = tp >> lg;
+    const int lg = 4 + std::rand() % 4, ppt = tp >> lg, pl = (tp == 128 ? 7 : 8) - lg;
     const int n_sink = round % 3 ? 0 : std::rand() % 300, window = round % 4 ? 0 : 1 + std::rand() % 2000;
     std::vector<int> len(B);
     for (int& n : len) n = std::rand() % (cap + 200) - 20;
@@ -30,7 +30,7 @@ int main() {
     std::vector<long long> first(B);
     for (int b = 0; b < B; ++b) {
       first[b] = total;
-      total += (long long)Hkv * (SeqTiles(len[b], cap, n_sink, window, lg, tp).count + kPairUnits);
+      total += (long long)Hkv * (SeqTiles(len[b], cap, n_sink, window, lg, pl).count + kPairUnits);
     }
     const Runs runs((int)total, n_cta);
     if (runs.begin(0) != 0 || runs.begin(n_cta) != total) return std::printf("runs do not cover\n"), 1;
@@ -43,7 +43,7 @@ int main() {
       while (u < end) {
         int b = 0;
         while (b + 1 < B && first[b + 1] <= u) ++b;
-        const SeqTiles s(len[b], cap, n_sink, window, lg, tp);
+        const SeqTiles s(len[b], cap, n_sink, window, lg, pl);
         const int units = s.count + kPairUnits, rem = (int)(u - first[b]);
         const int kvh = rem / units, t0 = rem % units;
         const size_t pair = (size_t)b * Hkv + kvh;
