@@ -308,17 +308,20 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float m) {
 
 // One block of the grid per touched (page, KV head) of K, and one of V, of page/8
 // warps with eight rows each.  The new rows are read once and stay in registers
-// between the block's amax and the encoding (eight rows a warp keep a thread within
-// 64 registers: sixteen rows, 128 registers, took 88 us where this takes 70; K and V
-// in one block, 76).  Other blocks rotate the queries.
+// between the block's amax and the encoding.  Eight rows a warp keep a thread within
+// 64 registers (sixteen rows and 128 registers: 88 us for a prefill of 4 x 4,096
+// tokens, 8 heads of 128, that takes 68 here).  It is bound by its instructions and by
+// the chain of small loads (offsets, length, table) that a block begins with: without
+// queries 30 us for 100 MB, 26 without the rotation, whose angles every head's block
+// reads again.  Other blocks rotate the queries.
 //
 // The pages that a sequence touches need no prefix sum: n tokens touch at most
 // n/page + 2 pages (rounded down), so sequence b owns items
 // [cu[b]/page + 2b, cu[b + 1]/page + 2(b + 1)) and the rest of them are idle.
 constexpr int kBlockRows = 8;  // rows a warp of the 8-bit append
 template <class E, int D>
-__global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendProblem p, int items,
-                                                              unsigned page_blocks, int NG) {
+__global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendProblem p,
+                                                                  unsigned q_per_item, int NG) {
   using T = typename E::T;
   constexpr int NC = D / 16;         // threads per row
   constexpr int RPP = 32 / NC;       // rows per pass of a warp
@@ -326,28 +329,28 @@ __global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendPro
   __shared__ float s_max[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   join_stream();
-  // page blocks and query blocks alternate, in proportion, so that one kind's
-  // waits lie under the other's traffic
-  const unsigned before = unsigned((unsigned long long)blockIdx.x * page_blocks / gridDim.x);
-  if (unsigned((blockIdx.x + 1ull) * page_blocks / gridDim.x) == before) {
+  const PagedView& c = p.c;
+  // an item's blocks: K and V of every head, then its share of the query blocks, so
+  // that one kind's waits lie under the other's traffic
+  const unsigned per_item = 2 * c.Hkv + q_per_item;
+  const unsigned item = blockIdx.x / per_item, part = blockIdx.x - item * per_item;
+  if (part >= 2u * c.Hkv) {
     const int per_token = NC * NG;
-    const long long t = (long long)(blockIdx.x - before) * (blockDim.x / per_token) +
+    const long long t = ((long long)item * q_per_item + (part - 2 * c.Hkv)) * (blockDim.x / per_token) +
                         threadIdx.x / per_token;
     const int i = threadIdx.x % per_token;
-    if (t < p.T && threadIdx.x / per_token < blockDim.x / per_token)
-      token_rows<E, D, 2>(p, (int)t, i % NC, i / NC, NG, false, lane);
+    if (t < p.T) token_rows<E, D, 2>(p, (int)t, i % NC, i / NC, NG, false, lane);
     return;
   }
-  const PagedView& c = p.c;
-  const bool is_v = before & 1;
-  const int item = (before >> 1) / c.Hkv, h = (before >> 1) % c.Hkv;
+  const bool is_v = part & 1;
+  const int h = part >> 1;
   // the sequence, and the new tokens [t0, t1) that fall in the item's page
   int b, c0, c1;
   if (p.cu) {
     int lo = 0, n = c.B;
     while (n > 1) {
       const int step = (n + 31) / 32, i = lane * step;
-      const bool le = i < n && (__ldg(p.cu + lo + i) >> c.page_log2) + 2 * (lo + i) <= item;
+      const bool le = i < n && (__ldg(p.cu + lo + i) >> c.page_log2) + 2 * (lo + i) <= (int)item;
       const int hit = __popc(__ballot_sync(0xffffffffu, le));
       const int skip = hit > 0 ? (hit - 1) * step : 0;
       lo += skip;
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendPro
   const int end = p.rope ? min(len, p.n_pos) : len;
   if ((start < 0 || end < len) && threadIdx.x == 0) set_status(c.status, SINKATTN_ERR_BOUNDS);
   const int first = start >> c.page_log2;  // page of the sequence's first new token
-  const int page_idx = first + (p.cu ? item - ((c0 >> c.page_log2) + 2 * b) : 0);
+  const int page_idx = first + (p.cu ? (int)item - ((c0 >> c.page_log2) + 2 * b) : 0);
   const int pos0 = page_idx << c.page_log2;  // position of the page's row 0
   const int r0 = max(start - pos0, 0), r1 = min(end - pos0, c.page_size);
   if (page_idx < max(first, 0) || r0 >= r1) return;
@@ -484,13 +487,14 @@ template <class E, int D>
 int append_fp8_typed(const PagedAppendProblem& p, cudaStream_t stream) {
   const int threads = p.c.page_size / kBlockRows * 32;
   const long long items = p.cu ? p.T / p.c.page_size + 2LL * p.c.B : p.c.B;
-  const long long pages = items * p.c.Hkv * 2;
   const int NG = 128 / D * 8;  // 64 threads a token: every block size holds whole tokens
   const int tokens = threads / (D / 16 * NG);
   const long long q_blocks = p.q ? (p.T + tokens - 1) / tokens : 0;
-  if (pages + q_blocks > 0x7fffffffLL) return SINKATTN_ERR_INVALID_ARG;
-  return launch_dependent(paged_append_fp8_kernel<E, D>, (unsigned)(pages + q_blocks), threads, stream,
-                          p, (int)items, (unsigned)pages, NG);
+  const long long q_per_item = (q_blocks + items - 1) / items;
+  const long long blocks = items * (2LL * p.c.Hkv + q_per_item);
+  if (blocks > 0x7fffffffLL) return SINKATTN_ERR_INVALID_ARG;
+  return launch_dependent(paged_append_fp8_kernel<E, D>, (unsigned)blocks, threads, stream, p,
+                          (unsigned)q_per_item, NG);
 }
 
 }  // namespace
