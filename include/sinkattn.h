@@ -458,9 +458,10 @@ typedef struct {
  *                  token's heads are contiguous, tokens k_stride / v_stride /
  *                  q_stride elements apart (multiples of 8; views of one fused
  *                  projection are fine).
- *   cu_new         device int32 [B + 1]: sequence b's new tokens are
- *                  [cu_new[b], cu_new[b + 1]); rows past cu_new[B] are ignored
- *                  and their outputs left as they are.  NULL: T = B, one token a
+ *   cu_new         device int32 [B + 1], not decreasing: sequence b's new tokens
+ *                  are [cu_new[b], cu_new[b + 1]); rows past cu_new[B] are
+ *                  ignored and their outputs left as they are.  A sequence whose
+ *                  offsets leave [0, T] is not written (SINKATTN_ERR_BOUNDS).  NULL: T = B, one token a
  *                  sequence, and a sequence with cache_seqlens[b] <= 0 has none.
  *                  The tokens are the sequence's last: the i-th of n has
  *                  position cache_seqlens[b] - n + i.
@@ -475,8 +476,8 @@ typedef struct {
  *   q_out          [T, Hq, D] contiguous (may be q itself); with q.
  *   k_out          [T, Hkv, D] contiguous or NULL: the rotated keys (for
  *                  sinkattn_fwd over the new tokens of a prefill).
- * A page that a call writes belongs to one sequence of the call (pages shared
- * for reading only may repeat). */
+ * A page that a call writes stands once in the call's tables (pages shared for
+ * reading only may repeat). */
 int sinkattn_paged_append(sinkattn_dtype dt, int T, int Hq, const sinkattn_paged_cache *cache,
                           const void *k, long long k_stride, const void *v, long long v_stride,
                           const void *q, long long q_stride, const int32_t *cu_new,

@@ -168,7 +168,11 @@ __device__ __forceinline__ Place place_token(const PagedAppendProblem& p, int t,
     const int b = find_sequence(p.cu, p.c.B, t, lane);
     const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
     if (t < c0 || t >= c1) return r;  // rows behind the last sequence
-    r.pos = __ldg(p.c.seqlens + b) - (c1 - t);
+    if (c0 < 0 || c1 > p.T) {         // offsets that leave the call's rows
+      set_status(p.c.status, SINKATTN_ERR_BOUNDS);
+      return r;
+    }
+    r.pos = max(__ldg(p.c.seqlens + b), 0) - (c1 - t);
     r.b = b;
   } else {
     const int n = __ldg(p.c.seqlens + t);
@@ -369,8 +373,12 @@ __global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendPro
     c1 = b + 1;
   }
   const int n_new = c1 - c0;
-  const int len = __ldg(c.seqlens + b);
-  if (n_new <= 0 || (!p.cu && len <= 0)) return;
+  const int len = max(__ldg(c.seqlens + b), 0);
+  if (n_new <= 0 || (!p.cu && len == 0)) return;
+  if (c0 < 0 || c1 > p.T) {  // offsets that leave the call's rows
+    if (threadIdx.x == 0) set_status(c.status, SINKATTN_ERR_BOUNDS);
+    return;
+  }
   const int start = len - n_new;  // position of token c0
   const int end = p.rope ? min(len, p.n_pos) : len;
   if ((start < 0 || end < len) && threadIdx.x == 0) set_status(c.status, SINKATTN_ERR_BOUNDS);
@@ -391,7 +399,7 @@ __global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendPro
     const int r = row_base + u * RPP + sub;
     const long long t = (long long)c0 + (pos0 + r - start);
     ua[u] = ub[u] = make_uint4(0, 0, 0, 0);
-    if (r >= r0 && r < r1 && t >= 0 && t < p.T) {
+    if (r >= r0 && r < r1) {
       ua[u] = *reinterpret_cast<const uint4*>(src + t * tstride + h * D + ch.a);
       ub[u] = *reinterpret_cast<const uint4*>(src + t * tstride + h * D + ch.b);
     }
@@ -406,7 +414,7 @@ __global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendPro
   for (int u = 0; u < PASSES; ++u) {
     const int r = row_base + u * RPP + sub;
     const long long t = (long long)c0 + (pos0 + r - start);
-    const bool on = r >= r0 && r < r1 && t >= 0 && t < p.T;
+    const bool on = r >= r0 && r < r1;
     widen8<E>(ua[u], xa[u]);
     widen8<E>(ub[u], xb[u]);
     if (on && ch.rot_a) {

@@ -684,6 +684,32 @@ def test_append_out_of_bounds_positions_write_nothing(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_append_offsets_past_the_tokens_write_nothing(fp8):
+    """Offsets that name rows past T, or before 0: the status is set, that sequence's
+    pages and scales stay as they are; the next ones are written.  So is a length
+    below the sequence's new tokens, down to the type's lowest."""
+    Hq, Hkv, D, page = 2, 1, 64, 16
+    c = append_case([3, 20, 4, 2], [5, 9, 0, 30], Hq, Hkv, D, page, BF, None, 48, fp8)
+    c["lens"][2] = -2 ** 31
+    f = lambda t: None if t is None else t.cuda()  # noqa: E731
+    call = S.paged_append_fp8 if fp8 else S.paged_append
+    x = c["x"].cuda()
+    for edit, T, bad in (([0, 3, 23, 27, 60], 29, [2, 3]), ([-1, 3, 23, 27, 29], 29, [0, 2]),
+                         ([0, 3, 23, 27, 29], 10, [1, 2, 3])):
+        cache = S.PagedCache(f(c["k"]), f(c["v"]), f(c["table"]), f(c["lens"]), f(c["ks"]), f(c["vs"]))
+        call(x[:T, Hq:Hq + Hkv], x[:T, Hq + Hkv:], cache, torch.tensor(edit, dtype=torch.int32).cuda())
+        torch.cuda.synchronize()
+        assert S.get_status() == 6
+        S.clear_status()
+        for b in range(4):
+            same = all(torch.equal(now[c["table"][b].long()].cpu(), was[c["table"][b].long()])
+                       for now, was in ((cache.k_pages, c["k"]), (cache.v_pages, c["v"]),
+                                        (cache.k_scale, c["ks"]), (cache.v_scale, c["vs"]))
+                       if was is not None)
+            assert same == (b in bad), (edit, b)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_the_calls_two_ways_agree(fp8):
     """A call with a stream argument takes the Python path, one without the short way
     through the extension; both allocate what is not given, and give the same bits."""
@@ -727,6 +753,37 @@ def test_append_many_sequences_and_no_token():
     torch.cuda.synchronize()
     wk, wv = oracle.paged_append(c["x"][:, 4:5], c["x"][:, 5:], c["table"], c["lens"], c["k"], c["v"], c["cu"])
     assert np.array_equal(np64(cache.k_pages), wk) and np.array_equal(np64(cache.v_pages), wv)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_the_largest_batch(fp8):
+    """65,535 sequences, some without a token: each block of the grid meets a run of
+    them.  A sequence's result does not depend on its neighbours."""
+    Hkv, D, page, B, n = 1, 64, 16, 65535, 64
+    g = gen(49)
+    x = torch.randn(n, 2 * Hkv + 2, D, generator=g).to(BF)
+    past = torch.randint(0, page, (n,), generator=g, dtype=torch.int32)
+    past[:3] = torch.tensor([0, page - 1, -1])
+    k, ks = make_pool(n, Hkv, page, D, None if fp8 else BF, g)
+    append = S.paged_append_fp8 if fp8 else S.paged_append
+    attend = S.paged_decode_fp8 if fp8 else S.paged_decode
+
+    def run(b):
+        i = torch.arange(b) % n
+        f = lambda t: None if t is None else t[i].cuda()  # noqa: E731
+        table = torch.arange(b, dtype=torch.int32).view(b, 1).cuda()
+        cache = S.PagedCache(f(k), f(k), table, f(past + 1), f(ks), f(ks))
+        xd = f(x)
+        append(xd[:, 2:3], xd[:, 3:], cache)
+        out = attend(xd[:, :2].contiguous(), cache, None)
+        torch.cuda.synchronize()
+        return [t.cpu() for t in (cache.k_pages, cache.v_pages, *out)], i
+
+    small, _ = run(n)
+    big, i = run(B)
+    assert not torch.equal(small[0], k) and bool((small[2] != 0).any())
+    for a, b in zip(small, big):
+        assert torch.equal(a[i], b)
 
 
 # ------------------------------------------------------------------ together
