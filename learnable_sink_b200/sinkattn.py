@@ -530,7 +530,8 @@ class PagedCache:
     codes (torch.float8_e4m3fn or uint8) with float32 scales ``k_scale`` /
     ``v_scale`` [n_pages, Hkv]; ``block_table`` int32 [B, max_pages] and
     ``cache_seqlens`` int32 [B], which counts a call's new tokens.  The tensors
-    are checked once, here, and kept; their contents may change between calls."""
+    are checked once, here, and kept: their contents may change between calls, the
+    attributes may not (other tensors are another PagedCache)."""
 
     __slots__ = ("k_pages", "v_pages", "block_table", "cache_seqlens", "k_scale", "v_scale",
                  "device", "B", "Hkv", "D", "_c", "_ref", "_dev", "_at", "_kind")
@@ -573,6 +574,13 @@ class PagedCache:
         self._ref = _c.byref(self._c)
         self._at = _c.addressof(self._c)
         self._kind = 2 if coded else int(k_pages.dtype == torch.float16)
+
+    def __setattr__(self, name, value):
+        # the calls read the descriptor that was built with the tensors: a tensor put
+        # in their place would go unseen
+        if hasattr(self, "_kind"):
+            raise AttributeError(f"PagedCache.{name} is fixed; build another PagedCache")
+        super().__setattr__(name, value)
 
 
 def _one_device(fn, *ts):

@@ -170,6 +170,16 @@ def caches(monkeypatch):
                 S.PagedCache(_pool(torch.uint8), _pool(torch.uint8), _table(), lens, sc, sc))
 
 
+def test_cache_attributes_are_fixed(caches):
+    """The calls use the addresses that the constructor checked: putting another tensor
+    in an attribute is refused, not ignored."""
+    for c in caches:
+        for name in ("cache_seqlens", "block_table", "k_pages", "k_scale", "B", "_kind"):
+            with pytest.raises(AttributeError, match=name):
+                setattr(c, name, torch.ones(B, dtype=i32))
+        assert c.cache_seqlens.tolist() == [0] * B
+
+
 def test_append_metadata_mismatches_are_refused(caches):
     c16, c8 = caches
     T = 7
