@@ -8,6 +8,7 @@ There is no fallback: if the library is missing or the device is not a B200
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -707,9 +708,19 @@ _APPEND = ("sinkattn_paged_append", "sinkattn_paged_append_fp8")
 _DECODE = ("sinkattn_paged_decode", "sinkattn_paged_decode_fp8")
 
 
+_AS_IS = contextlib.nullcontext()
+
+
+def _allocating(stream):
+    """What a call on `stream` allocates belongs to that stream: memory of the current
+    one may still be in use there, and would go back to it before the kernel ends."""
+    return _AS_IS if stream is None else torch.cuda.stream(stream)
+
+
 def _append_call(coded, k, v, cache, cu_new, rope, interleaved, q, q_out, k_out, stream):
     if q_out is None and q is not None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        with _allocating(stream):
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if stream is None:
         rc = (_short or _short_way()).paged_append(cache._at, coded, cache._kind, cache._dev, k, v,
                                                    cu_new, rope, interleaved, q, q_out, k_out)
@@ -750,15 +761,16 @@ def _decode_call(coded, q, cache, sink, n_sink, window, scale, stream, workspace
         if q.dim() != 3:
             raise SinkAttnError(_DECODE[coded], 1, "q must be [B, Hq, D]")
         B, Hq, D = q.shape
-        if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        if lse is None:
-            lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
-        if sink_s is None:
-            sink_s = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(max(paged_decode_workspace_bytes(B, Hq, cache.Hkv, D), 16),
-                                    dtype=torch.uint8, device=q.device)
+        with _allocating(stream):
+            if out is None:
+                out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            if lse is None:
+                lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+            if sink_s is None:
+                sink_s = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+            if workspace is None:
+                workspace = torch.empty(max(paged_decode_workspace_bytes(B, Hq, cache.Hkv, D), 16),
+                                        dtype=torch.uint8, device=q.device)
     if stream is None:
         rc = (_short or _short_way()).paged_decode(cache._at, coded, cache._kind, cache._dev, q, sink,
                                                    n_sink, window, scale, workspace, out, lse, sink_s)

@@ -739,6 +739,36 @@ def test_the_calls_two_ways_agree(fp8):
         attend(q, cache, None, window=-1)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_what_a_call_allocates_belongs_to_its_stream(fp8):
+    """Results and workspace of a call with a stream argument come from that stream's
+    memory: the current stream's could still be in use, or be given out again."""
+    Hq, Hkv, D, page = 4, 2, 64, 16
+    c = append_case([1, 1], [600, 5], Hq, Hkv, D, page, BF, None, 50, fp8)
+    f = lambda t: None if t is None else t.cuda()  # noqa: E731
+    cache = S.PagedCache(f(c["k"]), f(c["v"]), f(c["table"]), f(c["lens"]), f(c["ks"]), f(c["vs"]))
+    x = c["x"][:2].cuda()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    q = (S.paged_append_fp8 if fp8 else S.paged_append)(
+        x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], cache, q=x[:, :Hq], stream=side)
+    out = (S.paged_decode_fp8 if fp8 else S.paged_decode)(q, cache, None, stream=side)
+    side.synchronize()
+
+    def stream_of(t):
+        at = t.data_ptr()
+        return [s["stream"] for s in torch.cuda.memory_snapshot()
+                if s["address"] <= at < s["address"] + s["total_size"]]
+
+    assert stream_of(x) == [0]
+    for t in (q, *out):
+        assert stream_of(t) == [side.cuda_stream]
+    want = oracle.paged_decode(q, cache.k_pages, cache.v_pages, c["table"], c["lens"], 0, 0, None,
+                               D ** -0.5, *(None if t is None else t.cpu() for t in (cache.k_scale, cache.v_scale)))
+    tol = torch.finfo(BF).eps / 2 * np.abs(want[0]) + 2.0 ** -10 * 5
+    assert (np.abs(np64(out[0]) - want[0]) <= tol).all()
+
+
 def test_append_many_sequences_and_no_token():
     """More sequences than a warp's first search step covers, most without a token;
     T = 0 does nothing."""
