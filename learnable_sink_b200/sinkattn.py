@@ -693,6 +693,7 @@ def _paged_append(fn, call, coded, k, v, cache, cu_new, rope, interleaved, q, q_
         n_pos, rot = rope.shape
         if n_pos < 1 or rot % 16 or not 16 <= rot <= D:
             raise SinkAttnError(fn, 1, f"rot_dim {rot}: a multiple of 16 up to {D}")
+        n_pos = min(n_pos, 2 ** 31 - 1)  # no position lies past it
         rope_ptr = rope.data_ptr()
     if dev != torch.cuda.current_device():
         _current(fn, dev)
@@ -782,6 +783,13 @@ def _decode_call(coded, q, cache, sink, n_sink, window, scale, stream, workspace
                          window, scale, stream, workspace, out, lse, sink_s)
 
 
+def _int32(fn, name, x):
+    """ctypes would keep the low 32 bits of anything larger."""
+    if int(x) != x or not 0 <= x < 2 ** 31:
+        raise SinkAttnError(fn, 1, f"{name} {x}: a whole number in [0, 2^31)")
+    return int(x)
+
+
 def _paged_decode(fn, call, coded, q, cache, sink, n_sink, window, scale, stream, workspace, out,
                   lse, sink_s):
     if q.dim() != 3 or q.shape[0] != cache.B or q.shape[2] != cache.D:
@@ -807,10 +815,11 @@ def _paged_decode(fn, call, coded, q, cache, sink, n_sink, window, scale, stream
                                     ("workspace", workspace, workspace.shape, workspace.dtype)):
             if not _plain(t, want, kind, dev):
                 _refuse_plain(fn, name, t, want, kind, dev)
+    n_sink, window = _int32(fn, "n_sink", n_sink), _int32(fn, "window", window)
     if dev != torch.cuda.current_device():
         _current(fn, dev)
     rc = call(_CODE.get(dt) if dt in _CODE else _dt(q), Hq, D ** -0.5 if scale is None else float(scale),
-              q.data_ptr(), cache._ref, int(n_sink), int(window), None if sink is None else sink.data_ptr(),
+              q.data_ptr(), cache._ref, n_sink, window, None if sink is None else sink.data_ptr(),
               out.data_ptr(), lse.data_ptr(), sink_s.data_ptr(), workspace.data_ptr(),
               workspace.nbytes, _handle(stream, dev))
     if rc:

@@ -226,6 +226,15 @@ def test_decode_metadata_mismatches_are_refused(caches):
     _refused(lambda: S.paged_decode(q, c16, sink, workspace=ws, sink_s=torch.zeros(B, 1)), "sink_s")
 
 
+def test_decode_window_and_sink_tokens_out_of_range_are_refused(caches):
+    """Not cut to their low 32 bits (2^32 + 5 would see five positions)."""
+    q, z = torch.zeros(B, Hq, D, dtype=bf), torch.zeros(B, Hq)
+    for kw in (dict(window=2 ** 32 + 5), dict(n_sink=2 ** 32), dict(window=2 ** 31), dict(window=4.5),
+               dict(n_sink=-1), dict(window=-2 ** 32 + 7)):
+        for c, call in zip(caches, (S.paged_decode, S.paged_decode_fp8)):
+            _refused(lambda: call(q, c, None, workspace=z, out=q, lse=z, sink_s=z, **kw), "whole number")
+
+
 def test_short_way_declines_what_it_does_not_handle(caches):
     """The extension makes no call for tensors off the GPU, other objects, or values
     out of range: the Python path then says what is wrong."""
