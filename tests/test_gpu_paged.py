@@ -267,6 +267,32 @@ def test_decode_nan_in_a_visible_row_reaches_the_output(fp8):
     check_lse(np64(lse), want[1], 2.0 ** -12)
 
 
+@pytest.mark.parametrize("dtype", [BF, F16])
+def test_decode_infinity_in_a_visible_row(dtype):
+    """A value's reaches its own element of its heads, not as a finite number; a key's
+    takes all of the weight or none."""
+    clean = Problem([300, 100], 4, 2, 64, 16, dtype, seed=51)
+    want = clean.want()
+    p = Problem([300, 100], 4, 2, 64, 16, dtype, seed=51)
+    at = p.table[0, 3]
+    p.v[at, 1, 5, 7] = float("inf")
+    out, lse, ss = p.run()
+    assert not torch.isfinite(out[0, 2:, 7]).any()
+    out[0, 2:, 7] = torch.from_numpy(want[0][0, 2:, 7]).to(out)
+    p.check((out, lse, ss), want)
+    # scores of -inf: the row is as if it were masked; of +inf: NaN, as e^{inf - inf} is
+    p = Problem([300, 100], 4, 2, 64, 16, dtype, seed=51)
+    p.k[at, 1, 5, 7] = float("inf")
+    p.q[0, 2, 7], p.q[0, 3, 7] = -1.0, 1.0
+    out, lse, ss = p.run()
+    assert torch.isnan(out[0, 3]).all() and torch.isnan(lse[0, 3])
+    p.k[at, 1, 5, 7] = 0.0
+    p.k[at, 1, 5] = -256.0 * torch.sign(p.q[0, 2].float()).to(dtype)  # a score below -200
+    want = p.want()
+    rows = lambda a: np.concatenate([a[0, :3], a[1]])  # noqa: E731
+    p.check([torch.from_numpy(rows(np64(t))) for t in (out, lse, ss)], [rows(w) for w in want])
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_decode_shared_prefix_pages(fp8):
     """Several sequences read the same pages."""
