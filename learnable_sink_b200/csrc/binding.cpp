@@ -76,6 +76,13 @@ sinkattn_stream_t stream_of(int dev) {
       c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
 }
 
+// Other Python threads run while a launch waits for room in a stream's queue (what
+// the stream waits for may be theirs to do), as they do in a ctypes call.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // (descriptor, coded, kind, device, k, v, cu_new, rope, interleaved, q, q_out, k_out)
 int append(PyObject* const* a) {
   Cache c;
@@ -112,10 +119,12 @@ int append(PyObject* const* a) {
     rot = (int)rope->size(1);
   }
   if (T > INT_MAX || Hq > INT_MAX || c10::cuda::current_device() != c.dev) return kDeclined;
+  const sinkattn_stream_t stream = stream_of(c.dev);
+  const Unlocked unlocked;
   return g_append[c.coded](static_cast<sinkattn_dtype>(dt), (int)T, (int)Hq, c.c, data<void>(k), ks,
                            data<void>(v), vs, data<void>(q), qs, data<int32_t>(cu),
                            data<float>(rope), rot, n_pos, interleaved, data<void>(q_out),
-                           data<void>(k_out), stream_of(c.dev));
+                           data<void>(k_out), stream);
 }
 
 // (descriptor, coded, kind, device, q, sink, n_sink, window, scale, workspace, out, lse, sink_s)
@@ -147,10 +156,11 @@ int decode(PyObject* const* a) {
     scale = PyFloat_AsDouble(a[8]);
   }
   if (Hq > INT_MAX || c10::cuda::current_device() != c.dev) return kDeclined;
+  const sinkattn_stream_t stream = stream_of(c.dev);
+  const Unlocked unlocked;
   return g_decode[c.coded](static_cast<sinkattn_dtype>(dt), (int)Hq, (float)scale, data<void>(q), c.c,
                            (int)n_sink, (int)window, data<float>(sink), data<void>(out),
-                           data<float>(lse), data<float>(sink_s), data<void>(ws), ws->nbytes(),
-                           stream_of(c.dev));
+                           data<float>(lse), data<float>(sink_s), data<void>(ws), ws->nbytes(), stream);
 }
 
 // No C++ exception passes into the interpreter: what throws is declined (nothing

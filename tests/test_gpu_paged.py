@@ -15,6 +15,8 @@ Tolerances, from the arithmetic:
   2^-25 of the largest may be dropped).  The output is off by under
   2^-10 max|v|, plus its own rounding; LSE and the gate by under 2^-12.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -840,6 +842,49 @@ def test_the_largest_batch(fp8):
     assert not torch.equal(small[0], k) and bool((small[2] != 0).any())
     for a, b in zip(small, big):
         assert torch.equal(a[i], b)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_two_threads_at_once(fp8):
+    """Two Python threads, each with a stream, append to their own pages of one pool and
+    attend, step after step: the same bits as one after the other."""
+    Hq, Hkv, D, page, steps = 8, 2, 128, 16, 40
+    c = append_case([1] * 4, [300, 7, 1000, 40], Hq, Hkv, D, page, BF, None, 52, fp8)
+    width = c["table"].shape[1]
+    f = lambda t: None if t is None else t.clone().cuda()  # noqa: E731
+    xs = torch.randn(steps, 4, Hq + 2 * Hkv, D, generator=gen(53)).to(BF).cuda()
+    append = S.paged_append_fp8 if fp8 else S.paged_append
+    attend = S.paged_decode_fp8 if fp8 else S.paged_decode
+
+    def work(pools, half, got):
+        rows = slice(2 * half, 2 * half + 2)
+        with torch.cuda.stream(torch.cuda.Stream()):
+            lens = c["lens"][rows].cuda() - steps
+            lens.clamp_(min=0)
+            cache = S.PagedCache(pools[0], pools[1], c["table"][rows].contiguous().cuda(), lens, *pools[2:])
+            for i in range(steps):
+                x = xs[i, rows]
+                lens.add_(1)
+                q = append(x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], cache, q=x[:, :Hq])
+                got[half].append(attend(q, cache, None)[0])
+            torch.cuda.current_stream().synchronize()
+
+    res = []
+    for together in (False, True):
+        pools = [f(c["k"]), f(c["v"])] + ([f(c["ks"]), f(c["vs"])] if fp8 else [])
+        torch.cuda.synchronize()
+        got = [[], []]
+        threads = [threading.Thread(target=work, args=(pools, h, got)) for h in range(2)]
+        for t in threads:
+            t.start()
+            if not together:
+                t.join()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        assert len(got[0]) == len(got[1]) == steps and width >= 63
+        res.append([t.cpu() for t in [*got[0], *got[1], *pools]])
+    assert all(torch.equal(a, b) for a, b in zip(*res))
 
 
 # ------------------------------------------------------------------ together
