@@ -314,44 +314,52 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float m) {
   return encode4(a.x * m, a.y * m, b.x * m, b.y * m);
 }
 
-// One block of the grid per touched (page, KV head) of K, and one of V, of page/8
-// warps with eight rows each.  The new rows are read once and stay in registers
-// between the block's amax and the encoding.  Eight rows a warp keep a thread within
-// 64 registers (sixteen rows and 128 registers: 88 us for a prefill of 4 x 4,096
-// tokens, 8 heads of 128, that takes 68 here).  It is bound by its instructions and by
-// the chain of small loads (offsets, length, table) that a block begins with: without
-// queries 30 us for 100 MB, 26 without the rotation, whose angles every head's block
-// reads again.  Other blocks rotate the queries.
+// A block of the grid per touched page and KV head (D = 64: two heads) of K, and one
+// of V, of page/8 warps with eight rows each.  The new rows are read once and stay in
+// registers between the block's amax and the encoding: two passes of a warp over a
+// head of 128, or one over two heads of 64, which then share their angles and the
+// block's beginning.  That is what 64 registers hold.  A prefill of 4 x 4,096 tokens, 8
+// heads of 128, takes 68 us so, 88 with sixteen rows a warp (128 registers), 76 with
+// four rows of two heads; a ragged batch at D = 64 26 us, 28 with one head.  It is bound
+// by its instructions and by the chain of small loads (offsets, length, table) that a
+// block begins with: the prefill without queries takes 30 us for 100 MB, 26 without the
+// rotation, whose angles every head's block reads again.  Other blocks rotate the
+// queries.
 //
 // The pages that a sequence touches need no prefix sum: n tokens touch at most
 // n/page + 2 pages (rounded down), so sequence b owns items
 // [cu[b]/page + 2b, cu[b + 1]/page + 2(b + 1)) and the rest of them are idle.
-constexpr int kBlockRows = 8;  // rows a warp of the 8-bit append
+template <int D>
+struct BlockCfg {
+  static constexpr int HEADS = D == 128 ? 1 : 2;   // of a block
+  static constexpr int PASSES = D == 128 ? 2 : 1;  // of a warp
+  static constexpr int ROWS = PASSES * 32 / (D / 16);
+};
 template <class E, int D>
 __global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendProblem p,
                                                                   unsigned q_per_item, int NG) {
   using T = typename E::T;
   constexpr int NC = D / 16;         // threads per row
   constexpr int RPP = 32 / NC;       // rows per pass of a warp
-  constexpr int PASSES = kBlockRows / RPP;
-  __shared__ float s_max[32];
+  constexpr int PASSES = BlockCfg<D>::PASSES, HP = BlockCfg<D>::HEADS;
+  __shared__ float s_max[HP][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   join_stream();
   const PagedView& c = p.c;
   // an item's blocks: K and V of every head, then its share of the query blocks, so
   // that one kind's waits lie under the other's traffic
-  const unsigned per_item = 2 * c.Hkv + q_per_item;
+  const unsigned kv_blocks = 2 * ((c.Hkv + HP - 1) / HP), per_item = kv_blocks + q_per_item;
   const unsigned item = blockIdx.x / per_item, part = blockIdx.x - item * per_item;
-  if (part >= 2u * c.Hkv) {
+  if (part >= kv_blocks) {
     const int per_token = NC * NG;
-    const long long t = ((long long)item * q_per_item + (part - 2 * c.Hkv)) * (blockDim.x / per_token) +
+    const long long t = ((long long)item * q_per_item + (part - kv_blocks)) * (blockDim.x / per_token) +
                         threadIdx.x / per_token;
     const int i = threadIdx.x % per_token;
     if (t < p.T) token_rows<E, D, 2>(p, (int)t, i % NC, i / NC, NG, false, lane);
     return;
   }
   const bool is_v = part & 1;
-  const int h = part >> 1;
+  const int h0 = (part >> 1) * HP, nh = min(HP, c.Hkv - h0);  // its heads
   // the sequence, and the new tokens [t0, t1) that fall in the item's page
   int b, c0, c1;
   if (p.cu) {
@@ -388,84 +396,101 @@ __global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendPro
   const int r0 = max(start - pos0, 0), r1 = min(end - pos0, c.page_size);
   if (page_idx < max(first, 0) || r0 >= r1) return;
 
-  const int row_base = warp * kBlockRows;
+  const int row_base = warp * BlockCfg<D>::ROWS;
   const int j = lane % NC, sub = lane / NC;
   const Chunks ch = row_chunks<D>(j, is_v ? 0 : p.rot, p.interleaved);
   const T* src = is_v ? static_cast<const T*>(p.v) : static_cast<const T*>(p.k);
   const long long tstride = is_v ? p.v_stride : p.k_stride;
-  uint4 ua[PASSES], ub[PASSES];
+  uint4 ua[HP][PASSES], ub[HP][PASSES];
 #pragma unroll
   for (int u = 0; u < PASSES; ++u) {
     const int r = row_base + u * RPP + sub;
     const long long t = (long long)c0 + (pos0 + r - start);
-    ua[u] = ub[u] = make_uint4(0, 0, 0, 0);
-    if (r >= r0 && r < r1) {
-      ua[u] = *reinterpret_cast<const uint4*>(src + t * tstride + h * D + ch.a);
-      ub[u] = *reinterpret_cast<const uint4*>(src + t * tstride + h * D + ch.b);
+    const T* row = src + t * tstride + h0 * D;
+#pragma unroll
+    for (int e = 0; e < HP; ++e) {
+      ua[e][u] = ub[e][u] = make_uint4(0, 0, 0, 0);
+      if (r >= r0 && r < r1 && e < nh) {
+        ua[e][u] = *reinterpret_cast<const uint4*>(row + e * D + ch.a);
+        ub[e][u] = *reinterpret_cast<const uint4*>(row + e * D + ch.b);
+      }
     }
   }
   const int page = page_of(c, b, page_idx);  // looked up under the rows' loads
   if (page < 0) return;
-  float* scale_at = (is_v ? c.v_scale : c.k_scale) + (long long)page * c.Hkv + h;
-  const float s_old = r0 > 0 ? *scale_at : 0.f;
-  float xa[PASSES][8], xb[PASSES][8];
-  float amax = 0.f;
+  const long long blk = (long long)page * c.Hkv + h0;
+  float* scale_at = (is_v ? c.v_scale : c.k_scale) + blk;
+  float s_old[HP], amax[HP];
+#pragma unroll
+  for (int e = 0; e < HP; ++e) s_old[e] = r0 > 0 && e < nh ? scale_at[e] : 0.f;
+  float xa[HP][PASSES][8], xb[HP][PASSES][8];
+#pragma unroll
+  for (int e = 0; e < HP; ++e) amax[e] = 0.f;
 #pragma unroll
   for (int u = 0; u < PASSES; ++u) {
     const int r = row_base + u * RPP + sub;
-    const long long t = (long long)c0 + (pos0 + r - start);
     const bool on = r >= r0 && r < r1;
-    widen8<E>(ua[u], xa[u]);
-    widen8<E>(ub[u], xb[u]);
-    if (on && ch.rot_a) {
-      Angles an;
-      load_angles(an, p.rope, pos0 + r, p.rot, ch, p.interleaved);
-      rotate16<true>(xa[u], xb[u], an, ch, p.interleaved);
-    }
-    if (on && !is_v && p.k_out) {
-      T* ko = static_cast<T*>(p.k_out) + (t * c.Hkv + h) * D;
-      *reinterpret_cast<uint4*>(ko + ch.a) = pack8<E>(xa[u]);
-      *reinterpret_cast<uint4*>(ko + ch.b) = pack8<E>(xb[u]);
-    }
+    Angles an;
+    if (on && ch.rot_a) load_angles(an, p.rope, pos0 + r, p.rot, ch, p.interleaved);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(xa[u][i]), fabsf(xb[u][i])));
-  }
-  if (amax == INFINITY) {  // rare (a NaN has dropped out already): the finite ones alone
-    amax = 0.f;
-#pragma unroll
-    for (int u = 0; u < PASSES; ++u)
+    for (int e = 0; e < HP; ++e) {
+      widen8<E>(ua[e][u], xa[e][u]);
+      widen8<E>(ub[e][u], xb[e][u]);
+      if (on && ch.rot_a) rotate16<true>(xa[e][u], xb[e][u], an, ch, p.interleaved);
+      if (on && !is_v && p.k_out && e < nh) {
+        T* ko = static_cast<T*>(p.k_out) +
+                ((long long)(c0 + (pos0 + r - start)) * c.Hkv + h0 + e) * D;
+        *reinterpret_cast<uint4*>(ko + ch.a) = pack8<E>(xa[e][u]);
+        *reinterpret_cast<uint4*>(ko + ch.b) = pack8<E>(xb[e][u]);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        amax = fmaxf(amax, fmaxf(finite_abs(xa[u][i]), finite_abs(xb[u][i])));
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (lane == 0) s_max[warp] = amax;
-  __syncthreads();
-  amax = 0.f;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) amax = fmaxf(amax, s_max[w]);
-  const float s = fmaxf(block_scale(amax), s_old);
-  uint8_t* dst = static_cast<uint8_t*>(is_v ? c.v_pages : c.k_pages) +
-                 (((long long)page * c.Hkv + h) << c.page_log2) * D;
-  // where every value is 0 (or not finite) any factor will do
-  const float inv = s > 0.f ? __frcp_rn(s) : 1.f;
-  const bool grow = s > s_old && r0 > 0;
-  const float ratio = s_old * inv;
-#pragma unroll
-  for (int u = 0; u < PASSES; ++u) {
-    const int r = row_base + u * RPP + sub;
-    uint2* da = reinterpret_cast<uint2*>(dst + (long long)r * D + ch.a);
-    uint2* db = reinterpret_cast<uint2*>(dst + (long long)r * D + ch.b);
-    if (r >= r0 && r < r1) {
-      *da = encode8(xa[u], inv);
-      *db = encode8(xb[u], inv);
-    } else if (grow && r < r0) {
-      const uint2 a = *da, bq = *db;
-      *da = make_uint2(rescale4(a.x, ratio), rescale4(a.y, ratio));
-      *db = make_uint2(rescale4(bq.x, ratio), rescale4(bq.y, ratio));
+        amax[e] = fmaxf(amax[e], fmaxf(fabsf(xa[e][u][i]), fabsf(xb[e][u][i])));
     }
   }
-  if (lane == 0 && row_base == 0) *scale_at = s;
+#pragma unroll
+  for (int e = 0; e < HP; ++e) {
+    if (amax[e] == INFINITY) {  // rare (a NaN has dropped out already): the finite ones alone
+      amax[e] = 0.f;
+#pragma unroll
+      for (int u = 0; u < PASSES; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          amax[e] = fmaxf(amax[e], fmaxf(finite_abs(xa[e][u][i]), finite_abs(xb[e][u][i])));
+    }
+    // magnitudes are ordered as their bits are
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax[e]));
+    if (lane == 0) s_max[e][warp] = __uint_as_float(top);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < HP; ++e) {
+    if (e >= nh) break;
+    float top = 0.f;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) top = fmaxf(top, s_max[e][w]);
+    const float s = fmaxf(block_scale(top), s_old[e]);
+    uint8_t* dst = static_cast<uint8_t*>(is_v ? c.v_pages : c.k_pages) +
+                   ((blk + e) << c.page_log2) * D;
+    // where every value is 0 (or not finite) any factor will do
+    const float inv = s > 0.f ? __frcp_rn(s) : 1.f;
+    const bool grow = s > s_old[e] && r0 > 0;
+    const float ratio = s_old[e] * inv;
+#pragma unroll
+    for (int u = 0; u < PASSES; ++u) {
+      const int r = row_base + u * RPP + sub;
+      uint2* da = reinterpret_cast<uint2*>(dst + (long long)r * D + ch.a);
+      uint2* db = reinterpret_cast<uint2*>(dst + (long long)r * D + ch.b);
+      if (r >= r0 && r < r1) {
+        *da = encode8(xa[e][u], inv);
+        *db = encode8(xb[e][u], inv);
+      } else if (grow && r < r0) {
+        const uint2 a = *da, bq = *db;
+        *da = make_uint2(rescale4(a.x, ratio), rescale4(a.y, ratio));
+        *db = make_uint2(rescale4(bq.x, ratio), rescale4(bq.y, ratio));
+      }
+    }
+    if (threadIdx.x == 0) scale_at[e] = s;
+  }
 }
 
 template <class... A>
@@ -498,13 +523,14 @@ int append_typed(const PagedAppendProblem& p, cudaStream_t stream) {
 
 template <class E, int D>
 int append_fp8_typed(const PagedAppendProblem& p, cudaStream_t stream) {
-  const int threads = p.c.page_size / kBlockRows * 32;
+  const int threads = p.c.page_size / BlockCfg<D>::ROWS * 32;
   const long long items = p.cu ? p.T / p.c.page_size + 2LL * p.c.B : p.c.B;
   const int NG = 128 / D * 8;  // 64 threads a token: every block size holds whole tokens
   const int tokens = threads / (D / 16 * NG);
   const long long q_blocks = p.q ? (p.T + tokens - 1) / tokens : 0;
   const long long q_per_item = (q_blocks + items - 1) / items;
-  const long long blocks = items * (2LL * p.c.Hkv + q_per_item);
+  const long long kv_blocks = 2 * ((p.c.Hkv + BlockCfg<D>::HEADS - 1) / BlockCfg<D>::HEADS);
+  const long long blocks = items * (kv_blocks + q_per_item);
   if (blocks > 0x7fffffffLL) return SINKATTN_ERR_INVALID_ARG;
   return launch_dependent(paged_append_fp8_kernel<E, D>, (unsigned)blocks, threads, stream, p,
                           (unsigned)q_per_item, NG);

@@ -603,6 +603,33 @@ def test_append_fp8_scales_and_codes(dtype, D, page, rot, inter):
         assert np.array_equal(got[keep], want[keep])
 
 
+@pytest.mark.parametrize("Hkv", [1, 3, 8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_fp8_heads_do_not_touch_each_other(D, Hkv):
+    """Any number of heads gives each the bits that it gets alone, though blocks may hold
+    two; heads differ in size, so a neighbour's scale would show."""
+    page = 32
+    c = append_case(NEW, PAST, 0, Hkv, D, page, BF, D, 54 + Hkv, True)
+    c["x"] *= torch.exp2(torch.arange(2 * Hkv).float() * 3)[:, None].to(BF)
+    x, rope, cu = c["x"].cuda(), c["rope"].cuda(), c["cu"].cuda()
+    table, lens = c["table"].cuda(), c["lens"].cuda()
+
+    def run(heads):
+        pools = [c[n][:, heads].contiguous().cuda() for n in ("k", "v", "ks", "vs")]
+        cache = S.PagedCache(pools[0], pools[1], table, lens, *pools[2:])
+        k, v = x[:, :Hkv][:, heads].contiguous(), x[:, Hkv:][:, heads].contiguous()
+        k_out = torch.zeros_like(k)
+        S.paged_append_fp8(k, v, cache, cu, rope, k_out=k_out)
+        torch.cuda.synchronize()
+        return pools, k_out
+
+    pools, k_out = run(slice(0, Hkv))
+    for h in range(Hkv):
+        alone, k_alone = run(slice(h, h + 1))
+        assert all(torch.equal(a[:, h], b[:, 0]) for a, b in zip(pools, alone))
+        assert torch.equal(k_out[:, h], k_alone[:, 0])
+
+
 def test_append_fp8_special_values():
     """Infinities saturate and set no scale, NaN stays NaN, a block of zeros has
     scale 0 and grows later, tiny values take the smallest scale, and a value of
