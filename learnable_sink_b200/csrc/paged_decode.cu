@@ -8,8 +8,8 @@
 // heads of its KV head), as long as the arithmetic stays off the CUDA cores: 16
 // sequences of 8 to 32 thousand tokens, 8 KV heads of 128, take 206 us (6.5 TB/s, what a
 // plain copy reaches), 4 of 98 to 131 thousand in 8 bits 148 us (6.3 TB/s).  A call of
-// little work takes 8.5 us: 1 to find its place from the lengths, 1.6 until the first
-// scores, 1.5 for a tile and its result, 1 to end the kernel, 2.5 to join.  So
+// little work takes 7.9 us: 1 to find its place from the lengths, 1.6 until the first
+// scores, 1.5 for a tile and its result, 1 to end the kernel, 1.7 to join.  So
 // both products run on tcgen05 with the cache as the M side, where its rows lie
 // in shared memory as TMA brought them, whatever their type:
 //   S^T[128 positions x N] = K Q^T     A = K tile, K-major; B = Q, K-major
@@ -50,6 +50,7 @@ namespace {
 
 constexpr int kRows = 128;     // rows of a K or V tile
 constexpr int kHeads = 4;      // query heads per softmax warpgroup
+constexpr int kJoinThreads = 128;
 
 // ------------------------------------------------------------------ schedule
 template <int TP>  // positions per tile, 128 or 256
@@ -303,7 +304,7 @@ struct Bars {
   uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], q_free[2], drain;
 };
 
-// workspace: [B Hkv] (first CTA, segments), then the partials
+// workspace: [B Hkv] (first CTA, segments; B > kJoinThreads), then the partials
 __host__ __device__ inline size_t meta_floats(long long pairs) {
   return (size_t)((2 * pairs + 63) / 64 * 64);
 }
@@ -374,7 +375,6 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = tmem_s;
   const uint32_t tm_s = tmem, tm_o = tmem + 2 * NT;
 
@@ -421,6 +421,9 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
         }
       }
     } while (ok && w.next(p));
+    // The join's CTAs come up under the last tiles (let up at the start, the work before
+    // their wait is in this kernel's way: 0.2 to 0.4 us).
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!ok)  // leave no copy in flight
       for (int k = max(ld - SLOTS, 0); k < ld; ++k) {
         const long long t0 = clock64();
@@ -598,11 +601,12 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       };
       int id = load_id(0);
       if (w.t0 == 0 && lane == 0) {
-        // where the join finds the pair's segments
-        const long long pair = (long long)w.b * c.Hkv + w.kvh;
-        const int first = f0 + run - w.left;
-        reinterpret_cast<int2*>(p.part)[pair] = make_int2(
-            blockIdx.x, Runs(total, gridDim.x).cta_of(first + w.seq.count - 1) - (int)blockIdx.x + 1);
+        if (c.B > kJoinThreads) {  // where the join finds the pair's segments
+          const long long pair = (long long)w.b * c.Hkv + w.kvh;
+          const int first = f0 + run - w.left;
+          reinterpret_cast<int2*>(p.part)[pair] = make_int2(
+              blockIdx.x, Runs(total, gridDim.x).cta_of(first + w.seq.count - 1) - (int)blockIdx.x + 1);
+        }
         if (__ldg(c.seqlens + w.b) > w.seq.n) set_status(c.status, SINKATTN_ERR_BOUNDS);
       }
       for (int i = 0; i < w.cnt; ++i, ++j) {
@@ -883,23 +887,43 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
 }
 
 // Join a pair's segments and the sink: one CTA per (sequence, query head), a
-// thread a column.  Launched as a programmatic dependent.
-constexpr int kJoinThreads = 128;
-template <class E, int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodeProblem p) {
+// thread a column.  Launched as a programmatic dependent, which starts when every CTA
+// of the decode kernel is past its own wait: what earlier kernels wrote (lengths,
+// sinks) may be read at once, and where the pair's segments are is known before they
+// are done (0.5 to 1 us of a call).  With more sequences than threads, whose lengths
+// would take long to add up, the decode kernel's note says it.
+template <class E, int D, int TP>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodeProblem p, int ctas) {
   __shared__ float wt_s[kMaxCtas], red_s[2][4];
+  __shared__ int sum_s[4], before_s[4], mine_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, G = p.Hq / p.c.Hkv;
   const long long pair = (long long)b * p.c.Hkv + h / G;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const float a2 = p.sink ? __ldcg(p.sink + h) * kLog2e : -INFINITY;
+  int2 meta = make_int2(0, 0);
+  if (p.c.B <= kJoinThreads) {
+    const int units = tid < p.c.B ? seq_tiles<TP>(p, tid).count + kPairUnits : 0;
+    const int sum = __reduce_add_sync(0xffffffffu, units);
+    const int before = __reduce_add_sync(0xffffffffu, tid < b ? units : 0);
+    if (lane == 0) {
+      sum_s[warp] = sum;
+      before_s[warp] = before;
+    }
+    if (tid == b) mine_s = units;
+    __syncthreads();
+    const Runs runs((sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3]) * p.c.Hkv, ctas);
+    const int first = (before_s[0] + before_s[1] + before_s[2] + before_s[3]) * p.c.Hkv + h / G * mine_s;
+    meta.x = runs.cta_of(first);
+    meta.y = runs.cta_of(first + mine_s - kPairUnits - 1) - meta.x + 1;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int2 meta = __ldcg(reinterpret_cast<const int2*>(p.part) + pair);
+  if (p.c.B > kJoinThreads) meta = __ldcg(reinterpret_cast<const int2*>(p.part) + pair);
   const int ns = min(meta.y, kMaxCtas);
   if (ns <= 1) return;
   const float* parts = p.part + meta_floats((long long)p.c.B * p.c.Hkv);
   const long long step = (long long)G * (D + 2);
   const float* part = parts + (pair + meta.x) * step + (long long)(h % G) * (D + 2);
-  const float a2 = p.sink ? p.sink[h] * kLog2e : -INFINITY;
   // the first segments' columns are on their way while the weights are made
   constexpr int U = 16;
   float v[U];
@@ -995,7 +1019,7 @@ int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
   cfg.gridDim = dim3(c.B * p.Hq);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<E, D>, p) != cudaSuccess) return SINKATTN_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<E, D, G_::TP>, p, (int)grid) != cudaSuccess) return SINKATTN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA;
 }
 

@@ -147,6 +147,16 @@ def test_decode_many_short_sequences(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B", [128, 129])
+def test_decode_many_split_sequences(fp8, B):
+    """The join finds a pair's segments from the lengths, or with more sequences than it
+    has threads from the decode kernel's note: lengths of which most pairs are cut."""
+    lens = torch.randint(0, 900, (B,), generator=gen(55)).tolist()
+    lens[3], lens[B - 1] = 0, 5000
+    Problem(lens, 6, 3, 64, 32, BF, fp8, seed=56).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("bad", ["nan", "inf"])
 def test_decode_ignores_what_masked_rows_hold(fp8, bad):
     """Rows past the length, rows that the window hides, other pages and their
