@@ -43,6 +43,7 @@ struct PagedDecodeProblem {
   float* lse;
   float* sink_s;
   float* part;  // workspace
+  int lanes, chunks;  // KV heads that a group of CTAs works on side by side; Hkv / lanes
 };
 int launch_paged_decode(const PagedDecodeProblem& p, cudaStream_t stream);
 size_t paged_decode_part_floats(int B, int Hq, int Hkv, int D, int sms);
@@ -99,5 +100,23 @@ struct Runs {
     return unit < fat ? unit / (per + 1) : more + (unit - fat) / per;
   }
 };
+
+// CTAs work in groups, one KV head each of the same tiles: the largest divisor of Hkv
+// up to 8.
+constexpr int kMaxLanes = 8;
+__host__ __device__ inline int group_lanes(int Hkv) {
+  int n = Hkv < kMaxLanes ? Hkv : kMaxLanes;
+  while (Hkv % n != 0) --n;
+  return n;
+}
+
+// Whether every row of the schedule is left whole, to a group of its own (no partials, no
+// join), given the groups' even share: a cut costs two ends, and a lone CTA on an SM is
+// faster than two.  Break-even, measured over 4 to 37 equal sequences of 8 KV heads, lies
+// at rows longer by 3 to 4 units, and by 6 where two CTAs with a tile row a position
+// share an SM; 32 sequences of 1,024 tokens in 8 bits take 18 us so and 21 evenly cut.
+__host__ __device__ inline bool rows_whole(int rows, int longest, int share, int groups, int slack) {
+  return rows <= groups && longest <= share + share / 8 + (share + 3 < slack ? share + 3 : slack);
+}
 
 }  // namespace sk

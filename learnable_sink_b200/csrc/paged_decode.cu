@@ -6,10 +6,11 @@
 //
 // Bound by HBM (a visible row of K and V is read once and shared by the G query
 // heads of its KV head), as long as the arithmetic stays off the CUDA cores: 16
-// sequences of 8 to 32 thousand tokens, 8 KV heads of 128, take 206 us (6.5 TB/s, what a
-// plain copy reaches), 4 of 98 to 131 thousand in 8 bits 148 us (6.3 TB/s).  A call of
-// little work takes 7.9 us: 1 to find its place from the lengths, 1.6 until the first
-// scores, 1.5 for a tile and its result, 1 to end the kernel, 1.7 to join.  So
+// sequences of 8 to 32 thousand tokens, 8 KV heads of 128, take 195 to 202 us (6.6 to
+// 6.9 TB/s; a plain copy reaches 6.5), 4 of 98 to 131 thousand in 8 bits 139 to 143 us
+// (6.6 to 6.8 TB/s).  A call of little work takes 7.1 us: 1 to find its place from the
+// lengths, 1.6 until the first scores, 1.5 for a tile and its result, 1 to end the
+// kernel, 1.7 to join.  So
 // both products run on tcgen05 with the cache as the M side, where its rows lie
 // in shared memory as TMA brought them, whatever their type:
 //   S^T[128 positions x N] = K Q^T     A = K tile, K-major; B = Q, K-major
@@ -32,13 +33,19 @@
 // In the 8-bit cache the value scale goes into the probability: e^{x - m} is
 // multiplied by it in the exponent, with a reference of its own.
 //
-// Schedule: the tiles of every (sequence, KV head), in order, with a unit for the
-// pair's own cost behind them, are dealt in equal runs to the grid's CTAs; lengths are on the device, so every CTA adds them up
-// for itself.  A run is cut into segments where the pair changes.  A segment that
-// holds all of its pair writes the result; others write (O, m, l) at slot
-// pair + CTA, which no two segments share, and a second kernel joins them.
+// Schedule: CTAs work in groups of up to eight, one KV head each of the same tiles of
+// the same sequence, at about the same time: the heads' rows of a page are neighbours
+// in memory, and DRAM likes them together (the long calls above: 209 and 147 us if every
+// CTA goes its own way, 195 and 139 in groups of eight, 203 and 144 of four).  A row of
+// the schedule is a sequence's tiles for a group's heads, with a unit for the row's own
+// cost behind them; the rows, in order, are dealt in equal runs to the groups.  Lengths
+// are on the device, so every CTA adds them up for itself.  A run is cut into segments
+// where the row changes.  A segment that holds all of its row writes the result; others
+// write (O, m, l) at slot pair + first CTA of the group, which no two segments share, and
+// a second kernel joins them.  Rows of about the same length are left whole.
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <climits>
 
 #include "internal.h"
@@ -79,8 +86,8 @@ struct Walk {
     left -= seq.count + kPairUnits - t0;
     if (left <= 0) return false;
     t0 = 0;
-    if (++kvh == p.c.Hkv) {
-      kvh = 0;
+    if ((kvh += p.lanes) >= p.c.Hkv) {
+      kvh -= p.c.Hkv;
       seq = seq_tiles<TP>(p, ++b);
     }
     cut();
@@ -91,54 +98,80 @@ template <int TP>
 struct Start {
   Walk<TP> walk;
   int first, total;  // the run's first unit; units of all
+  bool whole;        // a pair a CTA
 };
 
 // Adds up the lengths (a slice of the sequences a thread) and finds where this
 // CTA's run begins; the thread whose slice it is in sets the walk up for all.
-template <int THREADS, int TP>
-__device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start<TP>* st, int* s_warp) {
+template <int THREADS, int TP, int SLACK>
+__device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start<TP>* st, int2* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per_thread = (p.c.B + THREADS - 1) / THREADS;
   const int b0 = tid * per_thread, b1 = min(b0 + per_thread, p.c.B);
-  int sum = 0;
-  for (int b = b0; b < b1; ++b) sum += seq_tiles<TP>(p, b).count + kPairUnits;
+  int sum = 0, longest = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int units = seq_tiles<TP>(p, b).count + kPairUnits;
+    sum += units;
+    longest = max(longest, units);
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
   int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31) s_warp[warp] = inc;
+  if (lane == 31) s_warp[warp] = make_int2(inc, longest);
   __syncthreads();
   int before = inc - sum, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
-    const int v = s_warp[w];
-    if (w < warp) before += v;
-    total += v;
+    const int2 v = s_warp[w];
+    if (w < warp) before += v.x;
+    total += v.x;
+    longest = max(longest, v.y);
   }
-  total *= p.c.Hkv;
-  before *= p.c.Hkv;
-  const Runs runs(total, gridDim.x);
-  const int f0 = runs.begin(blockIdx.x);
-  if (f0 >= before && f0 < before + sum * p.c.Hkv) {
+  const int chunks = p.chunks, group = blockIdx.y, groups = gridDim.y;
+  total *= chunks;
+  before *= chunks;
+  const Runs runs(total, groups);
+  if (rows_whole(p.c.B * chunks, longest, runs.per, groups, SLACK)) {
+    if (tid == 0) {
+      Walk<TP> w;
+      w.b = group / chunks;
+      w.kvh = (group - w.b * chunks) * p.lanes + blockIdx.x;
+      w.t0 = w.left = 0;
+      if (w.b < p.c.B) {
+        w.seq = seq_tiles<TP>(p, w.b);
+        w.left = w.seq.count + kPairUnits;
+        w.cut();
+      }
+      st->walk = w;
+      st->whole = true;
+    }
+    return;
+  }
+  const int f0 = runs.begin(group);
+  if (f0 >= before && f0 < before + sum * chunks) {
     Walk<TP> w;
     w.b = b0;
     for (;;) {
       w.seq = seq_tiles<TP>(p, w.b);
-      const int units = (w.seq.count + kPairUnits) * p.c.Hkv;
+      const int units = (w.seq.count + kPairUnits) * chunks;
       if (f0 < before + units) break;
       before += units;
       ++w.b;
     }
     const int rem = f0 - before, units = w.seq.count + kPairUnits;
-    w.kvh = rem / units;
-    w.t0 = rem - w.kvh * units;
-    w.left = runs.begin(blockIdx.x + 1) - f0;
+    const int chunk = rem / units;
+    w.kvh = chunk * p.lanes + blockIdx.x;
+    w.t0 = rem - chunk * units;
+    w.left = runs.begin(group + 1) - f0;
     w.cut();
     st->walk = w;
     st->first = f0;
     st->total = total;
+    st->whole = false;
   } else if (f0 == total && tid == 0) {
     st->walk.left = 0;  // less work than CTAs
   }
@@ -178,6 +211,7 @@ struct Geo {
   // CTAs an SM: one's segment ends and waits overlap the other's work.  32 KB tiles
   // (or sixteen heads) leave room for one.
   static constexpr int CTAS = TILE < 32768 && NWG < 4 ? 2 : 1;
+  static constexpr int SLACK = CTAS == 2 && PP == 1 ? 6 : 3;  // of rows_whole
   // A ring of tiles, K and V in turn.
   static constexpr int SLOTS =
       ((CTAS == 2 ? 112640 : 227328) - 2 * QBYTES - 2 * PBYTES - 1024) / TILE;
@@ -325,7 +359,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   __shared__ int abort_s;
   __shared__ uint32_t tmem_s;
   __shared__ Start<TP> start_s;
-  __shared__ int warp_s[G_::WARPS];
+  __shared__ int2 warp_s[G_::WARPS];
   __shared__ __align__(16) float qs_s[8][GP];  // query scales of the last eight segments
   __shared__ float sink_sm[8][GP];             // their sink logits, log2 units
   // (A segment's entries are read up to its result.  The queries of segment s + 8
@@ -371,7 +405,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   // up to here nothing that another kernel writes was read: this kernel is itself
   // a programmatic dependent, and its start lies under the end of the last one
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  find_start<G_::THREADS, TP>(p, &start_s, warp_s);
+  find_start<G_::THREADS, TP, G_::SLACK>(p, &start_s, warp_s);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -603,9 +637,10 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       if (w.t0 == 0 && lane == 0) {
         if (c.B > kJoinThreads) {  // where the join finds the pair's segments
           const long long pair = (long long)w.b * c.Hkv + w.kvh;
-          const int first = f0 + run - w.left;
+          const int first = f0 + run - w.left, group = blockIdx.y;
+          const Runs runs(total, gridDim.y);
           reinterpret_cast<int2*>(p.part)[pair] = make_int2(
-              blockIdx.x, Runs(total, gridDim.x).cta_of(first + w.seq.count - 1) - (int)blockIdx.x + 1);
+              group, start_s.whole ? 1 : runs.cta_of(first + w.seq.count - 1) - group + 1);
         }
         if (__ldg(c.seqlens + w.b) > w.seq.n) set_status(c.status, SINKATTN_ERR_BOUNDS);
       }
@@ -813,7 +848,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       named_bar_sync(1 + wg, 128);
       const long long pair = (long long)w.b * c.Hkv + w.kvh;
       const bool final = w.cnt == w.seq.count;
-      float* part = parts + (pair + blockIdx.x) * G * (D + 2);
+      float* part = parts + (pair + blockIdx.y * p.lanes) * G * (D + 2);
       const long long row0 = (long long)w.b * p.Hq + w.kvh * G;
       if (wt < H && h0 + wt < G) {
         const int h = h0 + wt;
@@ -892,10 +927,10 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
 // sinks) may be read at once, and where the pair's segments are is known before they
 // are done (0.5 to 1 us of a call).  With more sequences than threads, whose lengths
 // would take long to add up, the decode kernel's note says it.
-template <class E, int D, int TP>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodeProblem p, int ctas) {
+template <class E, int D, int TP, int SLACK>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodeProblem p, int groups) {
   __shared__ float wt_s[kMaxCtas], red_s[2][4];
-  __shared__ int sum_s[4], before_s[4], mine_s;
+  __shared__ int sum_s[4], before_s[4], longest_s[4], mine_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, G = p.Hq / p.c.Hkv;
   const long long pair = (long long)b * p.c.Hkv + h / G;
@@ -906,24 +941,32 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodePro
     const int units = tid < p.c.B ? seq_tiles<TP>(p, tid).count + kPairUnits : 0;
     const int sum = __reduce_add_sync(0xffffffffu, units);
     const int before = __reduce_add_sync(0xffffffffu, tid < b ? units : 0);
+    const int longest = __reduce_max_sync(0xffffffffu, units);
     if (lane == 0) {
       sum_s[warp] = sum;
       before_s[warp] = before;
+      longest_s[warp] = longest;
     }
     if (tid == b) mine_s = units;
     __syncthreads();
-    const Runs runs((sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3]) * p.c.Hkv, ctas);
-    const int first = (before_s[0] + before_s[1] + before_s[2] + before_s[3]) * p.c.Hkv + h / G * mine_s;
-    meta.x = runs.cta_of(first);
-    meta.y = runs.cta_of(first + mine_s - kPairUnits - 1) - meta.x + 1;
+    const int chunks = p.chunks;
+    const int total = (sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3]) * chunks;
+    const Runs runs(total, groups);
+    const int first = (before_s[0] + before_s[1] + before_s[2] + before_s[3]) * chunks +
+                      (chunks == 1 ? 0 : h / (G * p.lanes) * mine_s);
+    if (!rows_whole(p.c.B * chunks, max(max(longest_s[0], longest_s[1]), max(longest_s[2], longest_s[3])),
+                    runs.per, groups, SLACK)) {
+      meta.x = runs.cta_of(first);
+      meta.y = runs.cta_of(first + mine_s - kPairUnits - 1) - meta.x + 1;
+    }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (p.c.B > kJoinThreads) meta = __ldcg(reinterpret_cast<const int2*>(p.part) + pair);
   const int ns = min(meta.y, kMaxCtas);
   if (ns <= 1) return;
   const float* parts = p.part + meta_floats((long long)p.c.B * p.c.Hkv);
-  const long long step = (long long)G * (D + 2);
-  const float* part = parts + (pair + meta.x) * step + (long long)(h % G) * (D + 2);
+  const long long row = (long long)G * (D + 2), step = row * p.lanes;
+  const float* part = parts + pair * row + meta.x * step + (long long)(h % G) * (D + 2);
   // the first segments' columns are on their way while the weights are made
   constexpr int U = 16;
   float v[U];
@@ -960,7 +1003,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodePro
   __syncthreads();
   lt = (red_s[1][0] + red_s[1][1]) + (red_s[1][2] + red_s[1][3]);
   const float den = lt + ratio2(a2, mt);
-  const long long row = (long long)b * p.Hq + h;
+  const long long at = (long long)b * p.Hq + h;
   if (tid < D) {
     float o = 0.f;
     for (int i0 = 0; i0 < ns; i0 += U) {
@@ -968,16 +1011,16 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodePro
 #pragma unroll
       for (int u = 0; u < U; ++u) o += i0 + u < ns ? v[u] * wt_s[i0 + u] : 0.f;
     }
-    static_cast<typename E::T*>(p.out)[row * D + tid] = (typename E::T)(den != 0.f ? o / den : 0.f);
+    static_cast<typename E::T*>(p.out)[at * D + tid] = (typename E::T)(den != 0.f ? o / den : 0.f);
   }
   if (tid == 0) {
-    p.lse[row] = den != 0.f ? (mt + log2f(den)) * kLn2 : -INFINITY;
-    if (p.sink_s) p.sink_s[row] = den != 0.f ? lt / den : 0.f;
+    p.lse[at] = den != 0.f ? (mt + log2f(den)) * kLn2 : -INFINITY;
+    if (p.sink_s) p.sink_s[at] = den != 0.f ? lt / den : 0.f;
   }
 }
 
 template <class E, int D, bool F8, int NWG>
-int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
+int decode_cfg(PagedDecodeProblem p, cudaStream_t stream) {
   using G_ = Geo<E, D, F8, NWG>;
   const PagedView& c = p.c;
   const int rows = c.n_pages * c.Hkv * c.page_size;
@@ -995,12 +1038,13 @@ int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  // no more CTAs than the tables have tiles
+  // no more groups than the tables have units
   const long long tiles = ((long long)c.max_pages * c.page_size + G_::TP - 1) / G_::TP;
-  long long grid = tiles * c.B * c.Hkv;
   if ((tiles + kPairUnits) * c.B * c.Hkv > INT_MAX) return SINKATTN_ERR_UNSUPPORTED;
-  if (grid > G_::CTAS * sms) grid = G_::CTAS * sms;
-  if (grid > kMaxCtas) grid = kMaxCtas;
+  p.lanes = group_lanes(c.Hkv);
+  p.chunks = c.Hkv / p.lanes;
+  const long long groups =
+      std::min<long long>((tiles + kPairUnits) * c.B * p.chunks, std::min(G_::CTAS * sms, kMaxCtas) / p.lanes);
   record_start(SINKATTN_KERNEL_DECODE, stream);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -1009,7 +1053,7 @@ int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3(p.lanes, (unsigned)groups);
   cfg.blockDim = dim3(G_::THREADS);
   cfg.dynamicSmemBytes = G_::SMEM;
   const cudaError_t rc = cudaLaunchKernelEx(&cfg, kern, mk, mv, p);
@@ -1019,7 +1063,7 @@ int decode_cfg(const PagedDecodeProblem& p, cudaStream_t stream) {
   cfg.gridDim = dim3(c.B * p.Hq);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<E, D, G_::TP>, p, (int)grid) != cudaSuccess) return SINKATTN_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<E, D, G_::TP, G_::SLACK>, p, (int)groups) != cudaSuccess) return SINKATTN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA;
 }
 

@@ -157,6 +157,19 @@ def test_decode_many_split_sequences(fp8, B):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Hkv", [5, 9, 10, 11, 16])
+def test_decode_head_groups(fp8, Hkv):
+    """Heads that one group of blocks covers, several do, or that share no divisor with a
+    group: rows cut, rows of one length left whole, and more sequences than the join
+    adds up for itself."""
+    Problem([3000, 0, 1, 700, 2500], Hkv, Hkv, 64, 16, BF, fp8, seed=57).check()
+    Problem([600, 590, 600], 2 * Hkv, Hkv, 128, 32, BF, fp8, seed=58).check()
+    if Hkv == 10:
+        lens = torch.randint(0, 500, (129,), generator=gen(59)).tolist()
+        Problem(lens, Hkv, Hkv, 64, 64, BF, fp8, seed=60).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("bad", ["nan", "inf"])
 def test_decode_ignores_what_masked_rows_hold(fp8, bad):
     """Rows past the length, rows that the window hides, other pages and their
