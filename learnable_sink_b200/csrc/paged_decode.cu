@@ -37,12 +37,13 @@
 // the same sequence, at about the same time: the heads' rows of a page are neighbours
 // in memory, and DRAM likes them together (the long calls above: 209 and 147 us if every
 // CTA goes its own way, 195 and 139 in groups of eight, 203 and 144 of four; pages of 16
-// gain nothing).  A row of the schedule is a sequence's tiles for a group's heads, with a unit for the row's own
-// cost behind them; the rows, in order, are dealt in equal runs to the groups.  Lengths
-// are on the device, so every CTA adds them up for itself.  A run is cut into segments
-// where the row changes.  A segment that holds all of its row writes the result; others
-// write (O, m, l) at slot pair + first CTA of the group, which no two segments share, and
-// a second kernel joins them.  Rows of about the same length are left whole.
+// gain nothing).  A row of the schedule is a sequence's tiles for a group's heads, with
+// a unit for the row's own cost behind them; the rows, in order, are dealt in equal runs
+// to the groups.  Lengths are on the device, so every CTA adds them up for itself.  A run
+// is cut into segments where the row changes.  A segment that holds all of its row writes
+// the result; others write (O, m, l) at slot pair + first CTA of the group, which no two
+// segments share, and a second kernel joins them.  Rows of about the same length are left
+// whole.
 #include <cuda_fp8.h>
 
 #include <algorithm>
