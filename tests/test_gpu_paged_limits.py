@@ -1,0 +1,71 @@
+"""Paged cache on the GPU at the limits of its values: infinities through the rotation."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from learnable_sink_b200 import sinkattn as S
+
+from gpu_util import check_status
+from test_gpu_paged import BF, F16, gen
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _status():
+    S.clear_status()
+    yield
+    check_status()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (F16, 64)])
+def test_append_rotates_infinities(dtype, D, inter):
+    """An infinite key element makes both elements of its pair infinite: the sums that the
+    definition gives, +-448 s as codes and +-inf in k_out; NaN only where two infinities
+    cancel, or one meets a sine or cosine of 0.  The other elements are as without it."""
+    page, rot, n = 16, 32, 7
+    g = gen(70 + D + inter)
+    x = torch.randn(n, 2, D, generator=g).to(dtype)
+    x[:, :, 40] = 100.0  # past the rotated elements: the block's scale is 2^-2
+    clean = x.clone()
+    ia, ib = (6, 7) if inter else (3, 3 + rot // 2)
+    inf = float("inf")
+    for t, (a, b) in enumerate([(inf, 1.0), (inf, 1.0), (1.0, inf), (-inf, 1.0), (2.0, -inf), (-inf, inf)]):
+        x[t, 0, ia], x[t, 0, ib] = a, b
+    rope = torch.from_numpy(oracle.rope_table(n, rot)).float()
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    cu = torch.tensor([0, n], dtype=torch.int32).cuda()
+    table = torch.zeros(1, 1, dtype=torch.int32).cuda()
+    got = []
+    for src in (x, clean):
+        codes = torch.zeros(1, 1, page, D, dtype=torch.uint8)
+        c8 = S.PagedCache(codes.cuda(), codes.cuda(), table, lens, torch.zeros(1, 1).cuda(),
+                          torch.zeros(1, 1).cuda())
+        p16 = torch.zeros(1, 1, page, D, dtype=dtype)
+        c16 = S.PagedCache(p16.cuda(), p16.cuda(), table, lens)
+        k8, k16 = (torch.empty(n, 1, D, dtype=dtype, device="cuda") for _ in range(2))
+        xd = src.cuda()
+        S.paged_append_fp8(xd[:, :1], xd[:, 1:], c8, cu, rope.cuda(), inter, k_out=k8)
+        S.paged_append(xd[:, :1], xd[:, 1:], c16, cu, rope.cuda(), inter, k_out=k16)
+        torch.cuda.synchronize()
+        assert float(c8.k_scale) == 0.25
+        got.append((c8.k_pages[0, 0, :n].cpu(), k8[:, 0].cpu(), k16[:, 0].cpu()))
+    at = 6 // 2 if inter else 3  # the pair's angle
+    co, si = rope[:, at].double().numpy(), rope[:, rot // 2 + at].double().numpy()
+    a, b = x[:, 0, ia].double().numpy(), x[:, 0, ib].double().numpy()
+    with np.errstate(invalid="ignore"):
+        want = np.stack([a * co - b * si, b * co + a * si])
+    assert np.isnan(want).sum() == 2 and np.isinf(want).sum() == 10  # position 0's, and inf - inf
+    (codes, k8, k16), (codes0, k80, k160) = got
+    for i, w in zip((ia, ib), want):
+        for t in range(n):
+            c, o8, o16 = int(codes[t, i]), float(k8[t, i]), float(k16[t, i])
+            if np.isnan(w[t]):
+                assert c & 0x7F == 0x7F and np.isnan(o8) and np.isnan(o16), (t, i)
+            elif np.isinf(w[t]):
+                assert c == (0x7E if w[t] > 0 else 0xFE) and o8 == o16 == w[t], (t, i, c, o8, o16)
+    rest = [i for i in range(D) if i not in (ia, ib)]
+    for u, v in zip(got[0], got[1]):
+        assert torch.equal(u[:, rest], v[:, rest]) and torch.equal(u[6], v[6])
