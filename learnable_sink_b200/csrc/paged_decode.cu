@@ -30,6 +30,9 @@
 // and no shuffles.  Up to 16 heads take that many warpgroups, each with columns of
 // its own: a tile's time is latency, and four heads fit 80 registers, so the SM
 // holds enough warps to hide it (eight heads a thread: 1.6 times the time a tile).
+// Long sums are taken in two steps: the tensor cores truncate as they add, and a thread's
+// l takes a tile after the other, so every 64 tiles O and l are folded into sums that
+// are rounded (262,144 equal weights in one row: the result is 1.0e-3 too small without).
 // In the 8-bit cache the value scale goes into the probability: e^{x - m} is
 // multiplied by it in the exponent, with a reference of its own.
 //
@@ -207,7 +210,7 @@ struct Geo {
   static constexpr int PBYTES = NT / COLS * kRows * 16;
   static constexpr int QBYTES = N * CB;
   static constexpr int KE = 32 / EB;                   // K extent of an instruction
-  static constexpr int TMEM = 3 * NT <= 64 ? 64 : 3 * NT <= 128 ? 128 : 3 * NT <= 256 ? 256 : 512;
+  static constexpr int TMEM = 4 * NT;                  // two S^T, O^T and its folded sum
   static constexpr int WARPS = 4 * NWG + 4, THREADS = WARPS * 32;
   // CTAs an SM: one's segment ends and waits overlap the other's work.  32 KB tiles
   // (or sixteen heads) leave room for one.
@@ -226,6 +229,7 @@ struct Geo {
   static constexpr float TERM = F8 ? 32.f : (E::kFmt == 0 ? 2048.f : 1.f);
   static_assert((PT > QT ? PT : QT) * kHeads <= COLS, "a warpgroup's columns");
   static_assert(QBYTES % 1024 == 0 && TILE % 1024 == 0, "swizzled tiles start on their pattern");
+  static_assert(TMEM >= 32 && TMEM * CTAS <= 512 && (TMEM & (TMEM - 1)) == 0, "tensor memory");
   static_assert(SLOTS >= 3, "S of a tile goes ahead of P V of the last one");
 };
 
@@ -236,6 +240,10 @@ struct Geo {
 // of float32 (its last bit, 2^-24, lies below the third term's, 2^-20).  Where the
 // result is f16 too, what the first rounding to f16 left goes into the third term.
 constexpr float kLag = 2.f, kBase = 6.f;
+
+// Tiles whose sums O and l are held as the tensor cores and the threads add them up: at
+// most 512 steps of O, each truncated by less than 2^-23 of it.
+constexpr int kFold = 64;
 
 template <bool F8>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
@@ -370,6 +378,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   // were raised by last (a factor), each warp's maxima or sums, and the factors of
   // the result.
   __shared__ __align__(16) float ref_s[NWG][2][H], corr_s[NWG][2][H], red_s[NWG][4][2 * H], fac_s[NWG][H];
+  __shared__ float fold_s[NWG][4][H];  // each warp's folded l
   // a tile's pages: score factor and log2 of the value scale (NaN: outside the pool)
   __shared__ float2 page_s[2][TP / 16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -411,7 +420,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_s;
-  const uint32_t tm_s = tmem, tm_o = tmem + 2 * NT;
+  const uint32_t tm_s = tmem, tm_o = tmem + 2 * NT, tm_fold = tmem + 3 * NT;
 
   Walk<TP> w = start_s.walk;
   const int total = start_s.total, f0 = start_s.first, run = w.left;
@@ -515,7 +524,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
           if (i == w.cnt - 1) mma_commit(&bar.q_free[seg & 1]);
           if (pend >= 0) issue_pv();
           pend = j;
-          pend_first = i == 0;
+          pend_first = i % kFold == 0;
         }
         ++seg;
       } while (ok && w.next(p));
@@ -669,12 +678,26 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
     const int h0 = wg * H;                                    // its first query head
     const uint32_t my_lane = uint32_t(ww * 32) << 16;
     const uint32_t my_s = tm_s + wg * COLS + my_lane, my_o = tm_o + wg * COLS + my_lane;
+    const uint32_t my_fold = tm_fold + wg * COLS + my_lane;
     float(&ref)[2][H] = ref_s[wg];
     float(&corr)[2][H] = corr_s[wg];
     float(&red)[4][2 * H] = red_s[wg];
     const int ppt = TP >> c.page_log2;
     const long long pairs = (long long)c.B * c.Hkv;
     float* parts = p.part + meta_floats(pairs);
+    // l over the warp: lanes 8 h .. 8 h + 7 get head h's sum
+    auto warp_sums = [&](const float(&l)[H]) {
+      const bool hi = lane & 16, hj = lane & 8;
+      float a = hi ? l[2] : l[0], b = hi ? l[3] : l[1];
+      a += __shfl_xor_sync(0xffffffffu, hi ? l[0] : l[2], 16);
+      b += __shfl_xor_sync(0xffffffffu, hi ? l[1] : l[3], 16);
+      float t = hj ? b : a;
+      t += __shfl_xor_sync(0xffffffffu, hj ? a : b, 8);
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      return t;
+    };
+    float& my_fold_l = fold_s[wg][ww][lane >> 3];  // of lanes 0, 8, 16, 24
     int j = 0, seg = 0;
     // No wait that runs out breaks the loops (each returns at once after the
     // first): every thread meets every barrier, and the results are undefined.
@@ -683,6 +706,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
 #pragma unroll
       for (int h = 0; h < H; ++h) l[h] = 0.f;
       if (wt < 2 * H) ref[wt / H][wt % H] = kNone;
+      if ((lane & 7) == 0) my_fold_l = 0.f;
       for (int i = 0; i < w.cnt; ++i, ++j) {
         // the thread's positions (past the last page: past the sequence)
         const int at_page = (w.t0 + i) * ppt + (wt * PP >> c.page_log2);
@@ -691,6 +715,26 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
                                                : w.seq.n;
         mbar_wait(&bar.s_full[j & 1], (j >> 1) & 1, &abort_s, c.status);
         tc_fence_after();
+        if (i > 0 && i % kFold == 0) {  // rare: O starts afresh with this tile's product
+          mbar_wait(&bar.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, &abort_s, c.status);
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < PP; ++q) {
+            uint32_t r[COLS], f[COLS];
+            tmem_ld(my_o + q * N, r);
+            tmem_ld(my_fold + q * N, f);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < COLS; ++k)
+              r[k] = __float_as_uint(__uint_as_float(r[k]) + (i > kFold ? __uint_as_float(f[k]) : 0.f));
+            tmem_st(my_fold + q * N, r);
+          }
+          tmem_st_wait();
+          const float t = warp_sums(l);
+          if ((lane & 7) == 0) my_fold_l += t;
+#pragma unroll
+          for (int h = 0; h < H; ++h) l[h] = 0.f;
+        }
         const float2 page = page_s[j & 1][wt * PP >> c.page_log2];
         const bool held = !isnan(page.y);
         const float lvs = held ? page.y : 0.f;
@@ -733,7 +777,8 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
           if constexpr (F8) moves |= xm + (lvs - ref[1][h]) > kLag;
         }
         if (any_of_128(moves, wg)) {
-          // rare: raise the references to the maxima so far, and bring l and O along
+          // rare: raise the references to the maxima so far, and bring l, O and their
+          // folded sums along
           float mine = 0.f;
 #pragma unroll
           for (int h = 0; h < H; ++h) {
@@ -761,15 +806,18 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
             tc_fence_after();
 #pragma unroll
             for (int h = 0; h < H; ++h) l[h] *= corr[0][h];
+            if ((lane & 7) == 0) my_fold_l *= corr[0][lane >> 3];
+            for (uint32_t at = my_o; at <= (i < kFold ? my_o : my_fold); at += NT) {
 #pragma unroll
-            for (int q = 0; q < PP; ++q) {
-              uint32_t r[COLS];
-              tmem_ld(my_o + q * N, r);
-              tmem_ld_wait();
+              for (int q = 0; q < PP; ++q) {
+                uint32_t r[COLS];
+                tmem_ld(at + q * N, r);
+                tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < COLS; ++k)
-                r[k] = __float_as_uint(__uint_as_float(r[k]) * corr[F8][k % H]);
-              tmem_st(my_o + q * N, r);
+                for (int k = 0; k < COLS; ++k)
+                  r[k] = __float_as_uint(__uint_as_float(r[k]) * corr[F8][k % H]);
+                tmem_st(at + q * N, r);
+              }
             }
             tmem_st_wait();
           }
@@ -835,16 +883,9 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
         if (lane == 0) mbar_arrive(&bar.p_full[j & 1]);
       }
       // ------------------------------------------------ the segment's result
-      {  // l over the warp: lanes 8 h .. 8 h + 7 end with head h's sum
-        const bool hi = lane & 16, hj = lane & 8;
-        float a = hi ? l[2] : l[0], b = hi ? l[3] : l[1];
-        a += __shfl_xor_sync(0xffffffffu, hi ? l[0] : l[2], 16);
-        b += __shfl_xor_sync(0xffffffffu, hi ? l[1] : l[3], 16);
-        float t = hj ? b : a;
-        t += __shfl_xor_sync(0xffffffffu, hj ? a : b, 8);
-#pragma unroll
-        for (int o = 4; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        if ((lane & 7) == 0) red[ww][lane >> 3] = t;
+      {
+        const float t = warp_sums(l);
+        if ((lane & 7) == 0) red[ww][lane >> 3] = t + my_fold_l;
       }
       named_bar_sync(1 + wg, 128);
       const long long pair = (long long)w.b * c.Hkv + w.kvh;
@@ -882,6 +923,14 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       uint32_t r[COLS];
       tmem_ld(my_o + (PP == 2 ? (ww >> 1) * N : 0), r);
       tmem_ld_wait();
+      if (w.cnt > kFold) {
+        uint32_t f[COLS];
+        tmem_ld(my_fold + (PP == 2 ? (ww >> 1) * N : 0), f);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < COLS; ++k)
+          r[k] = __float_as_uint(__uint_as_float(r[k]) + __uint_as_float(f[k]));
+      }
       tc_fence_before();
       float o[H];
 #pragma unroll

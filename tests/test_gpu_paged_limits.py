@@ -1,4 +1,5 @@
-"""Paged cache on the GPU at the limits of its values: infinities through the rotation."""
+"""Paged cache on the GPU at the limits of its values: infinities through the rotation,
+long sums."""
 import numpy as np
 import pytest
 import torch
@@ -6,7 +7,7 @@ import torch
 import oracle
 from learnable_sink_b200 import sinkattn as S
 
-from gpu_util import check_status
+from gpu_util import check_lse, check_status, np64
 from test_gpu_paged import BF, F16, gen
 
 pytestmark = pytest.mark.gpu
@@ -69,3 +70,51 @@ def test_append_rotates_infinities(dtype, D, inter):
     rest = [i for i in range(D) if i not in (ia, ib)]
     for u, v in zip(got[0], got[1]):
         assert torch.equal(u[:, rest], v[:, rest]) and torch.equal(u[6], v[6])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 4), (128, 8)])
+def test_decode_sums_over_a_long_row(fp8, D, G):
+    """262,144 equal weights in a row that is not cut: the result is the values' mean, rounded
+    once.  The tensor cores truncate a sum as they add to it (less than 2^-23 of it for
+    each step of 16 positions), over 64 tiles of 128 positions at most: 2^-14; the tiles'
+    sums and the weights' own add 2^-19."""
+    n, page = 262144, 128
+    B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    pages = n // page
+    v = torch.rand(pages, 1, page, D, generator=torch.Generator("cuda").manual_seed(90), device="cuda") + 0.5
+    sc = ()
+    if fp8:
+        v = (v * 128).to(torch.float8_e4m3fn)
+        sc = (torch.full((pages, 1), 2.0 ** -7, device="cuda"),) * 2
+        value = v.double() * 2.0 ** -7
+    else:
+        v = v.to(F16)
+        value = v.double()
+    table = torch.arange(pages, dtype=torch.int32).expand(B, pages).contiguous().cuda()
+    cache = S.PagedCache(torch.zeros_like(v), v, table, torch.full((B,), n, dtype=torch.int32).cuda(), *sc)
+    call = S.paged_decode_fp8 if fp8 else S.paged_decode
+    out, lse, _ = call(torch.ones(B, G, D, dtype=F16, device="cuda"), cache, None)
+    want = value.mean((0, 1, 2))
+    d = (out.double() / want - 1).abs().max().item()
+    assert d <= 2.0 ** -11 + 2.0 ** -14 + 2.0 ** -18, d
+    check_lse(np64(lse), np.full((B, G), np.log(n)), 2.0 ** -18)
+
+
+@pytest.mark.parametrize("D,n_sink,window", [(64, 0, 0), (128, 0, 0), (64, 4, 40000)])
+def test_decode_lse_of_small_weights_beside_a_dominant_one(D, n_sink, window):
+    """The first token's weight is 1, every other one's 2^-20.3, in rows that are not cut: a
+    thread's sum begins with the large one, and the small ones must not be lost to it (64 of
+    them in a row lose at most 2^-18).  The scores are off by 2^-17.7 at most."""
+    n, page = 131072, 128
+    B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    k = torch.zeros(n // page, 1, page, D, dtype=BF, device="cuda")
+    k[0, 0, 0, 0] = 14.0
+    table = torch.arange(n // page, dtype=torch.int32).expand(B, n // page).contiguous().cuda()
+    cache = S.PagedCache(k, torch.zeros_like(k), table, torch.full((B,), n, dtype=torch.int32).cuda())
+    q = torch.zeros(B, 4, D, dtype=BF, device="cuda")
+    q[:, :, 0] = 8.0
+    lse = S.paged_decode(q, cache, None, n_sink=n_sink, window=window,
+                         scale=20.3 * float(np.log(2.0)) / 112.0)[1]
+    seen = n if window == 0 else window + n_sink
+    check_lse(np64(lse), np.full((B, 4), 20.3 * np.log(2.0) + np.log1p((seen - 1) * 2.0 ** -20.3)), 2.0 ** -16)
