@@ -516,7 +516,11 @@ int sinkattn_paged_append_fp8(sinkattn_dtype dt, int T, int Hq, const sinkattn_p
  *                  contents; not shared by calls that may overlap.
  * The work is divided over the GPU from the sequences' lengths on the device, so
  * a captured call stays balanced when they change.
- * sinkattn_paged_decode_fp8 -- the same over the 8-bit cache (q, out of type dt). */
+ * A weight e^(x - L) enters out with an error of at most 2^-16 of itself (f16:
+ * 2^-22, and 2^-40 of the sequence's largest).
+ * sinkattn_paged_decode_fp8 -- the same over the 8-bit cache (q, out of type dt).
+ * Here the product weight x page scale has an error of at most 2^-16 of itself and
+ * 2^-30 of the largest such product; lse and sink_s have no such floor. */
 size_t sinkattn_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int D);
 int sinkattn_paged_decode(sinkattn_dtype dt, int Hq, float scale, const void *q,
                           const sinkattn_paged_cache *cache, int n_sink, int window,

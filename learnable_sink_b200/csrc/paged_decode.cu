@@ -20,9 +20,10 @@
 // rounded terms t0 = r(x), t1 = r((x - t0) c), ..., each in columns of its own and
 // summed, with its factor, in float32.  E4M3 keeps four significant bits: two
 // terms hold a bf16 query exactly (three an f16 one) down to 2^-23 of its row's
-// largest; three terms hold a probability to 2^-12, falling to its last bit at
-// 2^-25 of the largest.  With a 16-bit cache the queries go in as they are and a
-// probability takes two terms (16 bits of it for bf16, 22 for f16).
+// largest; four terms hold a probability to 2^-16 of itself and 2^-30 of the largest
+// (with three, 2^-12 and 2^-26, a hundred thousand weights beside a dominant one went
+// missing from O, while l had them).  With a 16-bit cache the queries go in as they are
+// and a probability takes two terms (16 bits of it for bf16, 22 for f16).
 //
 // One thread owns one position of a tile and four query heads: softmax statistics
 // are per thread (l) or voted (the reference maximum moves, for all positions, when
@@ -201,7 +202,7 @@ struct Geo {
   static constexpr int QW = CB < 128 ? CB : 128;       // width of a query's rows
   static constexpr int TILE = kRows * RB;              // K or V tile
   static constexpr int QT = F8 ? (E::kFmt == 0 ? 3 : 2) : 1;  // terms of a query
-  static constexpr int PT = F8 ? 3 : 2;                // terms of a probability
+  static constexpr int PT = F8 ? 4 : 2;                // terms of a probability
   // A warpgroup's columns: term t of head h at 4 t + h of 16 bytes' worth, so that
   // a thread's probabilities are one 16-byte store.
   static constexpr int COLS = 16 / EB;
@@ -235,10 +236,12 @@ struct Geo {
 
 // Probabilities are held as 2^kBase e^{x - m}: with a reference that lags by at
 // most 2^kLag they stay within 2^8 (E4M3 reaches 448), as high as they can.  The
-// 8-bit terms are split in f16 pairs: its eleven bits are what three terms hold, a
-// residue and its move by 2^5 are exact in it, and it takes half the instructions
-// of float32 (its last bit, 2^-24, lies below the third term's, 2^-20).  Where the
-// result is f16 too, what the first rounding to f16 left goes into the third term.
+// 8-bit terms are split in f16 pairs, where a residue and its move by 2^5 are exact and
+// take half the instructions of float32.  What the rounding to f16 left is moved by 2^10
+// and goes into the third term, whose own residue is the fourth: at worst that is 512
+// and saturates, 64 2^-15 of a weight above 128, 2^-16 (a weight below its reference keeps
+// 2^-17.6).  The fourth term's last bit is 2^-24 in these units; half of it, and half of
+// that for f16's own subnormals, are below 2^-30 of the largest weight.
 constexpr float kLag = 2.f, kBase = 6.f;
 
 // Tiles whose sums O and l are held as the tensor cores and the threads add them up: at
@@ -837,15 +840,13 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
               e[k] = F8 ? fast_exp2(x[q][h + k] + (lvs - ref[1][h + k] + kBase)) : pr * 64.f;
             }
             if constexpr (F8) {
-              __half2 v = __floats2half2_rn(e[0], e[1]), rest{};
-              if constexpr (E::kFmt == 0) {
-                const float2 f = __half22float2(v);
-                rest = __floats2half2_rn((e[0] - f.x) * (G_::TERM * G_::TERM),
-                                         (e[1] - f.y) * (G_::TERM * G_::TERM));
-              }
+              __half2 v = __floats2half2_rn(e[0], e[1]);
+              const float2 f = __half22float2(v);
+              const __half2 rest = __floats2half2_rn((e[0] - f.x) * (G_::TERM * G_::TERM),
+                                                     (e[1] - f.y) * (G_::TERM * G_::TERM));
 #pragma unroll
               for (int t = 0; t < G_::PT; ++t) {
-                if (E::kFmt == 0 && t == G_::PT - 1) v = __hadd2(v, rest);
+                if (t == 2) v = __hadd2(v, rest);
                 const uint32_t two = e4m3x2_of_f16x2(v);
                 pk[t] = h == 0 ? two : __byte_perm(pk[t], two, 0x5410);
                 if (t + 1 < G_::PT)
@@ -935,9 +936,10 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       float o[H];
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        o[h] = __uint_as_float(r[h]) + __uint_as_float(r[H + h]) * (1.f / G_::TERM);
-        if constexpr (G_::PT == 3)
-          o[h] += __uint_as_float(r[2 * H + h]) * (1.f / (G_::TERM * G_::TERM));
+        o[h] = __uint_as_float(r[(G_::PT - 1) * H + h]);
+#pragma unroll
+        for (int t = G_::PT - 2; t >= 0; --t)
+          o[h] = __uint_as_float(r[t * H + h]) + o[h] * (1.f / G_::TERM);
       }
       if constexpr (PP == 2) {
         float4* half = reinterpret_cast<float4*>(sm + G_::OFF_P + wg * (kRows * 16)) + (wt & 63);

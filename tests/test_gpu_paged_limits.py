@@ -1,5 +1,5 @@
 """Paged cache on the GPU at the limits of its values: infinities through the rotation,
-long sums."""
+long sums, small weights."""
 import numpy as np
 import pytest
 import torch
@@ -11,6 +11,8 @@ from gpu_util import check_lse, check_status, np64
 from test_gpu_paged import BF, F16, gen
 
 pytestmark = pytest.mark.gpu
+
+KINDS = [(BF, False), (F16, False), (BF, True), (F16, True)]
 
 
 @pytest.fixture(autouse=True)
@@ -118,3 +120,49 @@ def test_decode_lse_of_small_weights_beside_a_dominant_one(D, n_sink, window):
                          scale=20.3 * float(np.log(2.0)) / 112.0)[1]
     seen = n if window == 0 else window + n_sink
     check_lse(np64(lse), np.full((B, 4), 20.3 * np.log(2.0) + np.log1p((seen - 1) * 2.0 ** -20.3)), 2.0 ** -16)
+
+
+@pytest.mark.parametrize("dtype,fp8", KINDS)
+@pytest.mark.parametrize("D,n_sink,window", [(64, 0, 0), (128, 0, 0), (64, 4, 40000)])
+@pytest.mark.parametrize("below,lift", [(20.3, 0), (23.7, 0), (25.5, 0), (27.5, 0), (20.3, 5)])
+def test_decode_small_weights_beside_a_dominant_one(dtype, fp8, D, n_sink, window, below, lift):
+    """The first token takes nearly all of the weight, every other one 2^-below of it, and
+    all share one reference: one or two equal sequences for each block that fits the GPU, so
+    that none is cut.  Values are 0 in the first token's page and 1 elsewhere, so the output is the
+    small weights' sum.  A weight is off by at most 2^-16 of itself and 2^-30 of the largest
+    (the latter times 2^lift, the first page's value scale over the others'); the result is
+    rounded once more; the sums of 64 tiles (2^-14), their own and the scores' errors add less
+    than 2^-12 of it."""
+    n, page = 131072, 128
+    B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    pages = n // page
+    k = torch.zeros(pages, 1, page, D, device="cuda")
+    v = torch.ones(pages, 1, page, D, device="cuda")
+    k[0, 0, 0, 0] = 14.0
+    v[0] = 0
+    sc = ()
+    if fp8:
+        k, v = (t.to(torch.float8_e4m3fn) for t in (k, v))
+        sc = (torch.ones(pages, 1, device="cuda"), torch.ones(pages, 1, device="cuda"))
+        sc[1][0] = 2.0 ** lift
+    else:
+        k, v = k.to(dtype), v.to(dtype)
+    table = torch.arange(pages, dtype=torch.int32).expand(B, pages).contiguous()
+    cache = S.PagedCache(k, v, table.cuda(), torch.full((B,), n, dtype=torch.int32).cuda(), *sc)
+    q = torch.zeros(B, 4, D, dtype=dtype)
+    q[:, :, 0] = 8.0
+    call = S.paged_decode_fp8 if fp8 else S.paged_decode
+    out, lse, ss = call(q.cuda(), cache, None, n_sink=n_sink, window=window,
+                        scale=below * float(np.log(2.0)) / 112.0)
+    torch.cuda.synchronize()
+    seen = n if window == 0 else window + n_sink
+    held = n - page if window == 0 else window  # those of value 1
+    w = 2.0 ** -below
+    want = held * w / (1 + (seen - 1) * w)
+    tol = want * (torch.finfo(dtype).eps / 2 + 2.0 ** -16 + 2.0 ** -12) + \
+        held * 2.0 ** -30 * (2.0 ** lift if fp8 else 1)
+    d = np.abs(np64(out) - want).max()
+    assert d <= tol, (d / want, tol / want)
+    # the score's float32 product is off by 2^-23 of `below` log2 units or so
+    check_lse(np64(lse), np.full((B, 4), below * np.log(2.0) + np.log1p((seen - 1) * w)), 2.0 ** -16)
+    assert np.abs(np64(ss) - 1).max() <= 2.0 ** -20
