@@ -339,9 +339,14 @@ __device__ __forceinline__ float warp_max(float x) {
 // The reference of a row that has seen nothing: low enough that every score
 // raises it, and finite, so that -inf minus it is -inf and not NaN.
 constexpr float kNone = -3e38f;
-// 2^(a - b), 0 from a = -inf (also over b = -inf)
+// 2^(a - b), 0 from a = -inf (also over b = -inf), 1 from a = b = inf (a sink logit's)
 __device__ __forceinline__ float ratio2(float a, float b) {
-  return a == -INFINITY ? 0.f : fast_exp2(a - b);
+  return a == -INFINITY ? 0.f : a == b ? 1.f : fast_exp2(a - b);
+}
+// log(lw 2^mt + e^a), den = lw + e^a / 2^mt: a itself, whatever its size, where the keys have
+// no weight beside it
+__device__ __forceinline__ float lse_of(float lw, float den, float mt, float a) {
+  return lw == 0.f ? a : (mt + log2f(den)) * kLn2;
 }
 
 template <int SLOTS>
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   __shared__ Start<TP> start_s;
   __shared__ int2 warp_s[G_::WARPS];
   __shared__ __align__(16) float qs_s[8][GP];  // query scales of the last eight segments
-  __shared__ float sink_sm[8][GP];             // their sink logits, log2 units
+  __shared__ float sink_sm[8][GP];             // their sink logits
   // (A segment's entries are read up to its result.  The queries of segment s + 8
   // are written once the scores of s + 6 are done, which follow the probabilities
   // of a tile behind segment s + 4.)
@@ -547,7 +552,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
     bool ok = true;
     do {
       uint8_t* qd = sm + G_::OFF_Q + (seg & 1) * G_::QBYTES;
-      const float a2 = p.sink && lane < G ? __ldg(p.sink + w.kvh * G + lane) * kLog2e : -INFINITY;
+      const float a = p.sink && lane < G ? __ldg(p.sink + w.kvh * G + lane) : -INFINITY;
       const typename E::T* q =
           static_cast<const typename E::T*>(p.q) + ((long long)w.b * p.Hq + w.kvh * G) * D + lane * CPL;
       auto at = [&](int r, int byte) {  // row r of the block, swizzled as the tiles are
@@ -570,7 +575,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       if (seg >= 2) ok = mbar_wait(&bar.q_free[seg & 1], ((seg >> 1) - 1) & 1, &abort_s, c.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (lane < GP) sink_sm[seg & 7][lane] = a2;
+      if (lane < GP) sink_sm[seg & 7][lane] = a;
 #pragma unroll
       for (int h = 0; h < GP; ++h) {
         if (h >= G) continue;
@@ -901,12 +906,12 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
         const float mo = F8 ? ref[1][wt] : m;
         float f;
         if (final) {
-          const float a2 = sink_sm[seg & 7][h];
+          const float a = sink_sm[seg & 7][h], a2 = a * kLog2e;
           const float mt = fmaxf(m, a2);
           const float lw = lt * ratio2(m, mt), den = lw + ratio2(a2, mt);
           const float inv = den != 0.f ? 1.f / den : 0.f;
           f = mo == kNone ? inv : fast_exp2(mo - mt - kBase) * inv;
-          p.lse[row0 + h] = den != 0.f ? (mt + log2f(den)) * kLn2 : -INFINITY;
+          p.lse[row0 + h] = lse_of(lw, den, mt, a);
           if (p.sink_s) p.sink_s[row0 + h] = lw * inv;
         } else {
           f = mo == kNone ? 1.f : fast_exp2(mo - m - kBase);
@@ -987,7 +992,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodePro
   const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, G = p.Hq / p.c.Hkv;
   const long long pair = (long long)b * p.c.Hkv + h / G;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const float a2 = p.sink ? __ldcg(p.sink + h) * kLog2e : -INFINITY;
+  const float a = p.sink ? __ldcg(p.sink + h) : -INFINITY, a2 = a * kLog2e;
   int2 meta = make_int2(0, 0);
   if (p.c.B <= kJoinThreads) {
     const int units = tid < p.c.B ? seq_tiles<TP>(p, tid).count + kPairUnits : 0;
@@ -1066,7 +1071,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodePro
     static_cast<typename E::T*>(p.out)[at * D + tid] = (typename E::T)(den != 0.f ? o / den : 0.f);
   }
   if (tid == 0) {
-    p.lse[at] = den != 0.f ? (mt + log2f(den)) * kLn2 : -INFINITY;
+    p.lse[at] = lse_of(lt, den, mt, a);
     if (p.sink_s) p.sink_s[at] = den != 0.f ? lt / den : 0.f;
   }
 }

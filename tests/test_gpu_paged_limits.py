@@ -1,5 +1,5 @@
 """Paged cache on the GPU at the limits of its values: infinities through the rotation,
-long sums, small weights."""
+long sums, small weights, sink logits of any size."""
 import numpy as np
 import pytest
 import torch
@@ -8,7 +8,7 @@ import oracle
 from learnable_sink_b200 import sinkattn as S
 
 from gpu_util import check_lse, check_status, np64
-from test_gpu_paged import BF, F16, gen
+from test_gpu_paged import BF, F16, Problem, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +166,22 @@ def test_decode_small_weights_beside_a_dominant_one(dtype, fp8, D, n_sink, windo
     # the score's float32 product is off by 2^-23 of `below` log2 units or so
     check_lse(np64(lse), np.full((B, 4), below * np.log(2.0) + np.log1p((seen - 1) * w)), 2.0 ** -16)
     assert np.abs(np64(ss) - 1).max() <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_sink_logits_of_any_size(fp8):
+    """A sink logit so large that the keys have no weight left, +inf among them, takes all of
+    it: out = 0, the gate 0, lse = a_h.  One so low that it has none is as no sink, and is
+    still lse where a sequence sees no key.  Whole sequences and split ones."""
+    top = float(torch.finfo(torch.float32).max)
+    a = [float("inf"), top, 3.0e38, 1e30, -top, -2.2e38, -1e30, -float("inf")]
+    p = Problem([9000, 100, 0], 8, 2, 128, 32, BF, fp8, seed=81)
+    p.sink = None
+    none = p.want()
+    p.sink = torch.tensor(a)
+    out, lse, ss = (t.cpu() for t in p.run())
+    sink = p.sink.expand(3, 8)
+    assert (out[:, :4] == 0).all() and (ss[:, :4] == 0).all()
+    assert torch.equal(lse[:, :4], sink[:, :4])
+    assert torch.equal(lse[2], sink[2]) and (out[2] == 0).all() and (ss[2] == 0).all()
+    p.check([t[:2, 4:] for t in (out, lse, ss)], [w[:2, 4:] for w in none])
