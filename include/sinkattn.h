@@ -472,7 +472,8 @@ typedef struct {
  *                  interleaved = 1; elements past rot_dim are copied.  rot_dim:
  *                  a multiple of 16 in [16, D].  Computed in float32, rounded
  *                  once.  A token whose position is >= n_pos or negative is not
- *                  written (SINKATTN_ERR_BOUNDS).
+ *                  written (SINKATTN_ERR_BOUNDS).  One whose page is out of
+ *                  bounds writes q_out alone, which does not need it.
  *   q_out          [T, Hq, D] contiguous (may be q itself); with q.
  *   k_out          [T, Hkv, D] contiguous or NULL: the rotated keys (for
  *                  sinkattn_fwd over the new tokens of a prefill).

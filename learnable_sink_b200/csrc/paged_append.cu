@@ -192,13 +192,14 @@ __device__ __forceinline__ Place place_token(const PagedAppendProblem& p, int t,
 // Copy or rotate the 16-bit rows of one token: rows [0, Hq) are its queries,
 // then Hkv keys, then Hkv values (only the queries when kv = false).  Thread
 // (j, g) of the token's D/16 x NG takes chunk pair j of rows g, g + NG, ...;
-// its angles are loaded once for all of them, and four rows are in flight.
+// its angles are loaded once for all of them, and four rows are in flight.  A token
+// whose page is not in the pool has its queries rotated all the same.
 template <class E, int D, int U>
 __device__ __forceinline__ void token_rows(const PagedAppendProblem& p, int t, int j, int g,
                                            int NG, bool kv, int lane) {
   using T = typename E::T;
   const int Hq = p.q ? p.Hq : 0, Hkv = p.c.Hkv;
-  const int rows = kv ? Hq + 2 * Hkv : Hq;
+  int rows = kv ? Hq + 2 * Hkv : Hq;
   const Chunks ch = row_chunks<D>(j, p.rot, p.interleaved);
   const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
   const T* k = static_cast<const T*>(p.k) + t * p.k_stride;
@@ -222,7 +223,7 @@ __device__ __forceinline__ void token_rows(const PagedAppendProblem& p, int t, i
   T* vdst = nullptr;
   if (kv) {
     const int page = page_of(p.c, pl.b, pl.pos >> p.c.page_log2);
-    if (page < 0) return;
+    if (page < 0) rows = Hq;
     const long long at =
         (((long long)page * Hkv << p.c.page_log2) + (pl.pos & (p.c.page_size - 1))) * D;
     kdst = static_cast<T*>(p.c.k_pages) + at;

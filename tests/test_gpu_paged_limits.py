@@ -1,5 +1,6 @@
 """Paged cache on the GPU at the limits of its values: infinities through the rotation,
-long sums, small weights, sink logits of any size."""
+long sums, small weights, sink logits of any size,
+bad pages."""
 import numpy as np
 import pytest
 import torch
@@ -8,7 +9,7 @@ import oracle
 from learnable_sink_b200 import sinkattn as S
 
 from gpu_util import check_lse, check_status, np64
-from test_gpu_paged import BF, F16, Problem, gen
+from test_gpu_paged import BF, F16, Problem, append_case, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -185,3 +186,51 @@ def test_decode_sink_logits_of_any_size(fp8):
     assert torch.equal(lse[:, :4], sink[:, :4])
     assert torch.equal(lse[2], sink[2]) and (out[2] == 0).all() and (ss[2] == 0).all()
     p.check([t[:2, 4:] for t in (out, lse, ss)], [w[:2, 4:] for w in none])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("single", [False, True])
+def test_append_with_a_bad_page_still_rotates_the_queries(fp8, single):
+    """A token whose page is outside the pool, or past the table, writes no key and no value,
+    nor k_out, and sets the status; its query, which needs the position alone, is rotated.
+    One without a valid position leaves all of its outputs as they were."""
+    Hq, Hkv, D, page = 4, 2, 64, 16
+    new = [1] * 5 if single else [2, 3, 1, 2, 1]
+    c = append_case(new, [20, 16, 3, 40, 70], Hq, Hkv, D, page, BF, 64, 80, fp8)
+    width = c["table"].shape[1]
+    c["table"][0, 1] = -1
+    c["table"][1, 1] = c["k"].shape[0]
+    c["lens"][3] = width * page + 1 if single else width * page + 2  # every new position is past the table
+    rope = torch.from_numpy(oracle.rope_table(width * page + 2, 64)).float()
+    c["lens"][4] = -7 if not single else width * page + 40  # below the new tokens; past the rotation table
+    T = sum(new)
+    x = c["x"][:T].cuda()
+    f = lambda t: None if t is None else t.cuda()  # noqa: E731
+    cache = S.PagedCache(f(c["k"]), f(c["v"]), f(c["table"]), f(c["lens"]), f(c["ks"]), f(c["vs"]))
+    q_out = torch.full((T, Hq, D), 7.0, dtype=BF, device="cuda")
+    k_out = torch.full((T, Hkv, D), 7.0, dtype=BF, device="cuda")
+    (S.paged_append_fp8 if fp8 else S.paged_append)(
+        x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], cache, None if single else c["cu"].cuda(), rope.cuda(),
+        q=x[:, :Hq], q_out=q_out, k_out=k_out)
+    torch.cuda.synchronize()
+    assert S.get_status() == 6
+    S.clear_status()
+    X = c["x"][:T].double().numpy()
+    cu, lens = c["cu"].tolist(), c["lens"].tolist()
+    touched = torch.zeros(c["k"].shape[0], dtype=torch.bool)
+    for b in range(5):
+        for t in range(cu[b], cu[b + 1]):
+            pos = lens[b] - (cu[b + 1] - t)
+            if b == 4:
+                assert (q_out[t] == 7).all() and (k_out[t] == 7).all()
+                continue
+            want = oracle.rotate(X[t:t + 1, :Hq], [pos], rope)[0]
+            assert (np.abs(np64(q_out[t]) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -18).all(), (b, t)
+            assert bool((k_out[t] == 7).all()) == (b != 2), (b, t)
+            if b == 2:
+                touched[c["table"][2, pos // page].long()] = True
+    for now, was in ((cache.k_pages, c["k"]), (cache.v_pages, c["v"]), (cache.k_scale, c["ks"]),
+                     (cache.v_scale, c["vs"])):
+        if was is not None:
+            assert torch.equal(now.cpu()[~touched], was[~touched])
+    assert not torch.equal(cache.v_pages.cpu()[touched], c["v"][touched])
