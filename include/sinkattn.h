@@ -461,8 +461,10 @@ typedef struct {
  *   cu_new         device int32 [B + 1], not decreasing: sequence b's new tokens
  *                  are [cu_new[b], cu_new[b + 1]); rows past cu_new[B] are
  *                  ignored and their outputs left as they are.  A sequence whose
- *                  offsets leave [0, T] is not written (SINKATTN_ERR_BOUNDS).  NULL: T = B, one token a
- *                  sequence, and a sequence with cache_seqlens[b] <= 0 has none.
+ *                  offsets leave [0, T] is not written (SINKATTN_ERR_BOUNDS; a
+ *                  call with T = 0 does nothing at all).  NULL: T = B, one
+ *                  token a sequence, and a sequence with cache_seqlens[b] <= 0
+ *                  has none.
  *                  The tokens are the sequence's last: the i-th of n has
  *                  position cache_seqlens[b] - n + i.
  *   rope           float32 [n_pos, rot_dim] or NULL (no rotation): cosines of

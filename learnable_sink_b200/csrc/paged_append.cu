@@ -160,6 +160,13 @@ __device__ __forceinline__ void join_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Offsets that leave the call's rows and may name none of them, so that no token's thread
+// meets them: one thread of the grid looks at the first and the last.
+__device__ __forceinline__ void check_offsets(const PagedAppendProblem& p) {
+  if (p.cu && blockIdx.x == 0 && threadIdx.x == 0 && (__ldg(p.cu) < 0 || __ldg(p.cu + p.c.B) > p.T))
+    set_status(p.c.status, SINKATTN_ERR_BOUNDS);
+}
+
 // Where a packed token goes.
 struct Place {
   int b, pos;  // b < 0: no sequence of the call has it, or it is out of bounds
@@ -282,6 +289,7 @@ __global__ void __launch_bounds__(kAppendThreads, AppendCfg<D>::BLOCKS)
   if (t >= p.T) return;
   const int i = threadIdx.x % per_token;
   token_rows<E, D, AppendCfg<D>::ROWS>(p, (int)t, i % NC, i / NC, NG, true, threadIdx.x & 31);
+  check_offsets(p);
 }
 
 // ---------------------------------------------------------------- 8-bit cache
@@ -348,6 +356,7 @@ __global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendPro
   __shared__ float s_max[HP][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   join_stream();
+  check_offsets(p);
   const PagedView& c = p.c;
   // an item's blocks: K and V of every head, then its share of the query blocks, so
   // that one kind's waits lie under the other's traffic

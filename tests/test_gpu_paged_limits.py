@@ -1,6 +1,6 @@
 """Paged cache on the GPU at the limits of its values: infinities through the rotation,
 long sums, small weights, sink logits of any size,
-bad pages."""
+bad pages and offsets."""
 import numpy as np
 import pytest
 import torch
@@ -234,3 +234,25 @@ def test_append_with_a_bad_page_still_rotates_the_queries(fp8, single):
         if was is not None:
             assert torch.equal(now.cpu()[~touched], was[~touched])
     assert not torch.equal(cache.v_pages.cpu()[touched], c["v"][touched])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("offsets,bad", [([0, 3, 5, 9], [2]), ([0, 5, 5, 6], [2]), ([-4, -1, 2, 5], [0, 1]),
+                                         ([0, 2, 4, 2 ** 31 - 1], [2])])
+def test_append_offsets_wholly_outside_set_the_status(fp8, offsets, bad):
+    """Offsets that reach past T or below 0 set the status even where no row of the call is
+    theirs; the sequences inside are written."""
+    c = append_case([2, 2, 1], [8, 10, 25], 2, 1, 64, 16, BF, None, 82, fp8)
+    f = lambda t: None if t is None else t.cuda()  # noqa: E731
+    cache = S.PagedCache(f(c["k"]), f(c["v"]), f(c["table"]), f(c["lens"]), f(c["ks"]), f(c["vs"]))
+    x = c["x"][:5].cuda()
+    (S.paged_append_fp8 if fp8 else S.paged_append)(
+        x[:, 2:3], x[:, 3:], cache, torch.tensor(offsets, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert S.get_status() == 6
+    S.clear_status()
+    for b in range(3):
+        rows = c["table"][b].long()
+        same = torch.equal(cache.v_pages.cpu()[rows], c["v"][rows])
+        n = offsets[b + 1] - offsets[b]
+        assert same == (b in bad or n == 0), b
