@@ -18,6 +18,16 @@ struct PagedView {
   int* status;
 };
 
+// The paged kernels may be on an SM while the kernel before them still writes what they
+// read behind their wait (lengths, tables, scales, queries, even a rotation table): the
+// read-only path, __ldg, is for what nobody writes while a kernel lives, and is not used.
+// Plain loads cost the same.  Scales, of which other blocks write the neighbours in a
+// sector, come from L2 (in the decode; all of these from L2 cost an 8-bit prefill 14 %).
+template <class T>
+__device__ __forceinline__ T fresh(const T* p) {
+  return *p;
+}
+
 struct PagedAppendProblem {
   PagedView c;
   int dt, T, Hq, D, rot, n_pos, interleaved;

@@ -30,7 +30,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int t, in
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int i = lane * step;
-    const bool le = i < n && __ldg(cu + lo + i) <= t;
+    const bool le = i < n && fresh(cu + lo + i) <= t;
     const int hit = __popc(__ballot_sync(0xffffffffu, le));
     const int skip = hit > 0 ? (hit - 1) * step : 0;
     lo += skip;
@@ -44,7 +44,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int t, in
 __device__ __forceinline__ int page_of(const PagedView& c, int b, int page_idx) {
   int id = -1;
   if (page_idx >= 0 && page_idx < c.max_pages)
-    id = __ldg(c.table + (long long)b * c.max_pages + page_idx);
+    id = fresh(c.table + (long long)b * c.max_pages + page_idx);
   if (id < 0 || id >= c.n_pages) {
     set_status(c.status, SINKATTN_ERR_BOUNDS);
     return -1;
@@ -91,8 +91,8 @@ __device__ __forceinline__ void load_angles(Angles& t, const float* rope, long l
     const int at = interleaved ? (i ? ch.b : ch.a) / 2 : ch.a + 4 * i;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
     if (i ? ch.rot_b : ch.rot_a) {
-      x = __ldg(reinterpret_cast<const float4*>(row + at));
-      y = __ldg(reinterpret_cast<const float4*>(row + rot / 2 + at));
+      x = fresh(reinterpret_cast<const float4*>(row + at));
+      y = fresh(reinterpret_cast<const float4*>(row + rot / 2 + at));
     }
     t.c[4 * i] = x.x; t.c[4 * i + 1] = x.y; t.c[4 * i + 2] = x.z; t.c[4 * i + 3] = x.w;
     t.s[4 * i] = y.x; t.s[4 * i + 1] = y.y; t.s[4 * i + 2] = y.z; t.s[4 * i + 3] = y.w;
@@ -163,7 +163,7 @@ __device__ __forceinline__ void join_stream() {
 // Offsets that leave the call's rows and may name none of them, so that no token's thread
 // meets them: one thread of the grid looks at the first and the last.
 __device__ __forceinline__ void check_offsets(const PagedAppendProblem& p) {
-  if (p.cu && blockIdx.x == 0 && threadIdx.x == 0 && (__ldg(p.cu) < 0 || __ldg(p.cu + p.c.B) > p.T))
+  if (p.cu && blockIdx.x == 0 && threadIdx.x == 0 && (fresh(p.cu) < 0 || fresh(p.cu + p.c.B) > p.T))
     set_status(p.c.status, SINKATTN_ERR_BOUNDS);
 }
 
@@ -175,16 +175,16 @@ __device__ __forceinline__ Place place_token(const PagedAppendProblem& p, int t,
   Place r{-1, 0};
   if (p.cu) {
     const int b = find_sequence(p.cu, p.c.B, t, lane);
-    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
+    const int c0 = fresh(p.cu + b), c1 = fresh(p.cu + b + 1);
     if (t < c0 || t >= c1) return r;  // rows behind the last sequence
     if (c0 < 0 || c1 > p.T) {         // offsets that leave the call's rows
       set_status(p.c.status, SINKATTN_ERR_BOUNDS);
       return r;
     }
-    r.pos = max(__ldg(p.c.seqlens + b), 0) - (c1 - t);
+    r.pos = max(fresh(p.c.seqlens + b), 0) - (c1 - t);
     r.b = b;
   } else {
-    const int n = __ldg(p.c.seqlens + t);
+    const int n = fresh(p.c.seqlens + t);
     if (n <= 0) return r;  // a slot without a new token
     r.pos = n - 1;
     r.b = t;
@@ -378,22 +378,22 @@ __global__ void __launch_bounds__(512, 2) paged_append_fp8_kernel(PagedAppendPro
     int lo = 0, n = c.B;
     while (n > 1) {
       const int step = (n + 31) / 32, i = lane * step;
-      const bool le = i < n && (__ldg(p.cu + lo + i) >> c.page_log2) + 2 * (lo + i) <= (int)item;
+      const bool le = i < n && (fresh(p.cu + lo + i) >> c.page_log2) + 2 * (lo + i) <= (int)item;
       const int hit = __popc(__ballot_sync(0xffffffffu, le));
       const int skip = hit > 0 ? (hit - 1) * step : 0;
       lo += skip;
       n = min(step, n - skip);
     }
     b = lo;
-    c0 = __ldg(p.cu + b);
-    c1 = __ldg(p.cu + b + 1);
+    c0 = fresh(p.cu + b);
+    c1 = fresh(p.cu + b + 1);
   } else {
     b = item;
     c0 = b;
     c1 = b + 1;
   }
   const int n_new = c1 - c0;
-  const int len = max(__ldg(c.seqlens + b), 0);
+  const int len = max(fresh(c.seqlens + b), 0);
   if (n_new <= 0 || (!p.cu && len == 0)) return;
   if (c0 < 0 || c1 > p.T) {  // offsets that leave the call's rows
     if (threadIdx.x == 0) set_status(c.status, SINKATTN_ERR_BOUNDS);

@@ -66,9 +66,13 @@ constexpr int kJoinThreads = 128;
 
 // ------------------------------------------------------------------ schedule
 template <int TP>  // positions per tile, 128 or 256
+__device__ __forceinline__ SeqTiles tiles_of(const PagedDecodeProblem& p, int len) {
+  return SeqTiles(len, p.c.max_pages << p.c.page_log2, p.n_sink, p.window, p.c.page_log2,
+                  (TP == 128 ? 7 : 8) - p.c.page_log2);
+}
+template <int TP>
 __device__ __forceinline__ SeqTiles seq_tiles(const PagedDecodeProblem& p, int b) {
-  return SeqTiles(__ldg(p.c.seqlens + b), p.c.max_pages << p.c.page_log2, p.n_sink, p.window,
-                  p.c.page_log2, (TP == 128 ? 7 : 8) - p.c.page_log2);
+  return tiles_of<TP>(p, fresh(p.c.seqlens + b));
 }
 __device__ __forceinline__ bool visible(const PagedDecodeProblem& p, int n, int pos) {
   return pos < n && (p.window <= 0 || pos < p.n_sink || pos >= n - p.window);
@@ -446,7 +450,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
         const int k = (w.t0 + i) * ppt + lane;
         int id = -1;
         if (lane < ppt && i < w.cnt && k < w.seq.pages)
-          id = __ldg(c.table + (long long)w.b * c.max_pages + w.seq.page(k));
+          id = fresh(c.table + (long long)w.b * c.max_pages + w.seq.page(k));
         return id < c.n_pages ? id : -1;
       };
       int next = load_id(0);
@@ -552,7 +556,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
     bool ok = true;
     do {
       uint8_t* qd = sm + G_::OFF_Q + (seg & 1) * G_::QBYTES;
-      const float a = p.sink && lane < G ? __ldg(p.sink + w.kvh * G + lane) : -INFINITY;
+      const float a = p.sink && lane < G ? fresh(p.sink + w.kvh * G + lane) : -INFINITY;
       const typename E::T* q =
           static_cast<const typename E::T*>(p.q) + ((long long)w.b * p.Hq + w.kvh * G) * D + lane * CPL;
       auto at = [&](int r, int byte) {  // row r of the block, swizzled as the tiles are
@@ -565,11 +569,11 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       for (int h = 0; h < GP; ++h) {  // every head's loads in flight at once
         if (h >= G) continue;
         if constexpr (CPL == 4) {
-          const uint2 u = __ldg(reinterpret_cast<const uint2*>(q + h * D));
+          const uint2 u = fresh(reinterpret_cast<const uint2*>(q + h * D));
           raws[h][0] = u.x;
           raws[h][CPL / 2 - 1] = u.y;
         } else {
-          raws[h][0] = __ldg(reinterpret_cast<const uint32_t*>(q + h * D));
+          raws[h][0] = fresh(reinterpret_cast<const uint32_t*>(q + h * D));
         }
       }
       if (seg >= 2) ok = mbar_wait(&bar.q_free[seg & 1], ((seg >> 1) - 1) & 1, &abort_s, c.status);
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
         const int k = (w.t0 + i) * ppt + lane;
         int id = -2;  // no page here
         if (lane < ppt && i < w.cnt && k < w.seq.pages) {
-          id = __ldg(c.table + (long long)w.b * c.max_pages + w.seq.page(k));
+          id = fresh(c.table + (long long)w.b * c.max_pages + w.seq.page(k));
           if (id < 0 || id >= c.n_pages) {
             set_status(c.status, SINKATTN_ERR_BOUNDS);
             id = -1;
@@ -660,14 +664,14 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
           reinterpret_cast<int2*>(p.part)[pair] = make_int2(
               group, start_s.whole ? 1 : runs.cta_of(first + w.seq.count - 1) - group + 1);
         }
-        if (__ldg(c.seqlens + w.b) > w.seq.n) set_status(c.status, SINKATTN_ERR_BOUNDS);
+        if (fresh(c.seqlens + w.b) > w.seq.n) set_status(c.status, SINKATTN_ERR_BOUNDS);
       }
       for (int i = 0; i < w.cnt; ++i, ++j) {
         float2 v = make_float2(scale_log2, 1.f);
         if (F8 && id >= 0) {
           const long long blk = (long long)id * c.Hkv + w.kvh;
-          v.x *= __ldg(c.k_scale + blk);
-          v.y = __ldg(c.v_scale + blk);
+          v.x *= __ldcg(c.k_scale + blk);
+          v.y = __ldcg(c.v_scale + blk);
         }
         const bool outside = id == -1;
         id = load_id(i + 1);
@@ -981,7 +985,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
 // Join a pair's segments and the sink: one CTA per (sequence, query head), a
 // thread a column.  Launched as a programmatic dependent, which starts when every CTA
 // of the decode kernel is past its own wait: what earlier kernels wrote (lengths,
-// sinks) may be read at once, and where the pair's segments are is known before they
+// sinks) may be read at once, from L2, and where the pair's segments are is known before they
 // are done (0.5 to 1 us of a call).  With more sequences than threads, whose lengths
 // would take long to add up, the decode kernel's note says it.
 template <class E, int D, int TP, int SLACK>
@@ -995,7 +999,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodePro
   const float a = p.sink ? __ldcg(p.sink + h) : -INFINITY, a2 = a * kLog2e;
   int2 meta = make_int2(0, 0);
   if (p.c.B <= kJoinThreads) {
-    const int units = tid < p.c.B ? seq_tiles<TP>(p, tid).count + kPairUnits : 0;
+    const int units = tid < p.c.B ? tiles_of<TP>(p, __ldcg(p.c.seqlens + tid)).count + kPairUnits : 0;
     const int sum = __reduce_add_sync(0xffffffffu, units);
     const int before = __reduce_add_sync(0xffffffffu, tid < b ? units : 0);
     const int longest = __reduce_max_sync(0xffffffffu, units);

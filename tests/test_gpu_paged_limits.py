@@ -1,6 +1,6 @@
 """Paged cache on the GPU at the limits of its values: infinities through the rotation,
-long sums, small weights, sink logits of any size,
-bad pages and offsets."""
+long sums, small weights, sink logits of any size, bad pages and offsets; chains of steps in
+which an 8-bit block's scale grows."""
 import numpy as np
 import pytest
 import torch
@@ -9,7 +9,7 @@ import oracle
 from learnable_sink_b200 import sinkattn as S
 
 from gpu_util import check_lse, check_status, np64
-from test_gpu_paged import BF, F16, Problem, append_case, gen
+from test_gpu_paged import BF, F16, Problem, append_case, gen, make_pool, make_table
 
 pytestmark = pytest.mark.gpu
 
@@ -256,3 +256,52 @@ def test_append_offsets_wholly_outside_set_the_status(fp8, offsets, bad):
         same = torch.equal(cache.v_pages.cpu()[rows], c["v"][rows])
         n = offsets[b + 1] - offsets[b]
         assert same == (b in bad or n == 0), b
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 32)])
+def test_steps_whose_scales_grow(D, page):
+    """Append and attend step after step without a wait, values half as large again each
+    step, so that blocks are re-encoded to a larger scale under the kernel before: each
+    step's result belongs to that step's codes and scales."""
+    Hq, Hkv, steps = 16, 8, 24
+    past = [0, page - 3, 200]
+    g = gen(83)
+    table, n = make_table([p + steps for p in past], page, g)
+    k, ks = make_pool(n, Hkv, page, D, None, g)
+    v, vs = make_pool(n, Hkv, page, D, None, g)
+    lens = torch.tensor(past, dtype=torch.int32)
+    xs = torch.randn(steps, 3, Hq + 2 * Hkv, D, generator=g)
+    xs[:, :, Hq:] *= 1.5 ** torch.arange(steps).float()[:, None, None, None] * 0.01
+    xs = xs.to(BF)
+    sink = torch.randn(Hq, generator=g)
+    cache = S.PagedCache(k.cuda(), v.cuda(), table.cuda(), lens.cuda(), ks.cuda(), vs.cuda())
+    xd, sd, one = xs.cuda(), sink.cuda(), torch.ones(3, dtype=torch.int32, device="cuda")
+    ws = torch.empty(S.paged_decode_workspace_bytes(3, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+    qs = xd[:, :, :Hq].contiguous()
+    torch.cuda.synchronize()
+    got = []
+    for i in range(steps):
+        cache.cache_seqlens.add_(one)
+        S.paged_append_fp8(xd[i, :, Hq:Hq + Hkv], xd[i, :, Hq + Hkv:], cache)
+        got.append(S.paged_decode_fp8(qs[i], cache, sd, workspace=ws))
+    torch.cuda.synchronize()
+    kc, vc, ksn, vsn = k.numpy(), v.numpy(), ks.double().numpy(), vs.double().numpy()
+    grown = 0
+    for i in range(steps):
+        lens = lens + 1
+        was = vsn
+        kc, ksn = oracle.paged_append_fp8(xs[i, :, Hq:Hq + Hkv], table, lens, kc, ksn)
+        vc, vsn = oracle.paged_append_fp8(xs[i, :, Hq + Hkv:], table, lens, vc, vsn)
+        grown += int((vsn > was).sum())
+        want = oracle.paged_decode(xs[i, :, :Hq], kc, vc, table, lens, 0, 0, sink, D ** -0.5, ksn, vsn)
+        top = (np.abs(oracle.fp8_e4m3_value(vc)) * vsn[:, :, None, None])[table.numpy()].max()
+        kmax = (np.abs(oracle.fp8_e4m3_value(kc)) * ksn[:, :, None, None])[table.numpy()].max()
+        qsum = xs[i, :, :Hq].abs().double().sum(-1).max().item()
+        # the error of a score's D float32 products, and a weight's, twice that
+        err = (D + 3) * 2.0 ** -24 * qsum * kmax * D ** -0.5
+        d = np.abs(np64(got[i][0]) - want[0])
+        assert (d <= 2.0 ** -8 * np.abs(want[0]) + (2.0 ** -10 + 2 * err) * top).all(), i
+        check_lse(np64(got[i][1]), want[1], 2.0 ** -12 + err)
+    assert grown > 100
+    assert np.array_equal(cache.k_pages.cpu().numpy(), kc) and np.array_equal(np64(cache.k_scale), ksn)
+    assert np.array_equal(cache.v_pages.cpu().numpy(), vc) and np.array_equal(np64(cache.v_scale), vsn)
