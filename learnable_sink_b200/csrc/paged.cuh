@@ -129,4 +129,85 @@ __host__ __device__ inline bool rows_whole(int rows, int longest, int share, int
   return rows <= groups && longest <= share + share / 8 + (share + 3 < slack ? share + 3 : slack);
 }
 
+// Groups of a grid of at most `ctas` CTAs: no more than the tables have units.
+__host__ __device__ inline int schedule_groups(long long units, int ctas, int lanes) {
+  const int most = (ctas < kMaxCtas ? ctas : kMaxCtas) / lanes;
+  return units < most ? (int)units : most;
+}
+
+// A row of the schedule is a sequence's tiles for a chunk of `lanes` KV heads.  A CTA's
+// run of units is walked segment by segment; seq_of(b) gives the tiles of sequence b.
+struct Walk {
+  int b, kvh, t0, cnt;  // the segment: tiles [t0, t0 + cnt) of (b, kvh)
+  SeqTiles seq;
+  int left;             // units of the run from the segment on
+  __host__ __device__ void cut() { cnt = seq.count - t0 < left ? seq.count - t0 : left; }
+  // a run that begins behind a row's tiles begins with the next row
+  template <class F>
+  __host__ __device__ bool begin(int Hkv, int lanes, F seq_of) {
+    return left > 0 && (cnt > 0 || next(Hkv, lanes, seq_of));
+  }
+  template <class F>
+  __host__ __device__ bool next(int Hkv, int lanes, F seq_of) {
+    left -= seq.count + kPairUnits - t0;
+    if (left <= 0) return false;
+    t0 = 0;
+    if ((kvh += lanes) >= Hkv) {
+      kvh -= Hkv;
+      seq = seq_of(++b);
+    }
+    cut();
+    return true;
+  }
+};
+// The run of CTA `lane` of a group that has row `group` to itself (none: left = 0).
+template <class F>
+__host__ __device__ inline Walk whole_walk(int group, int lane, int B, int lanes, int chunks,
+                                           F seq_of) {
+  Walk w;
+  w.b = group / chunks;
+  w.kvh = (group - w.b * chunks) * lanes + lane;
+  w.t0 = w.left = 0;
+  if (w.b < B) {
+    w.seq = seq_of(w.b);
+    w.left = w.seq.count + kPairUnits;
+    w.cut();
+  }
+  return w;
+}
+// The run of `units` units from f0 on, which lies at or behind unit `before`, the first of
+// sequence b.
+template <class F>
+__host__ __device__ inline Walk cut_walk(int f0, int units, int b, int before, int lane, int lanes,
+                                         int chunks, F seq_of) {
+  Walk w;
+  w.b = b;
+  for (;;) {
+    w.seq = seq_of(w.b);
+    const int of_all = (w.seq.count + kPairUnits) * chunks;
+    if (f0 < before + of_all) break;
+    before += of_all;
+    ++w.b;
+  }
+  const int rem = f0 - before, row = w.seq.count + kPairUnits;
+  const int chunk = rem / row;
+  w.kvh = chunk * lanes + lane;
+  w.t0 = rem - chunk * row;
+  w.left = units;
+  w.cut();
+  return w;
+}
+// Groups that have a part of a row's tiles, whose first unit `first` lies in group `group`.
+__host__ __device__ inline int parts_of(const Runs& runs, int group, int first, int tiles) {
+  return runs.cta_of(first + tiles - 1) - group + 1;
+}
+// Partials of pair (b, kvh) = b Hkv + kvh: rows come in order along the groups, so no two
+// segments share a slot.
+__host__ __device__ inline long long part_slot(long long pair, int group, int lanes) {
+  return pair + group * lanes;
+}
+__host__ __device__ inline long long part_slots(long long pairs, int sms) {
+  return pairs + (2 * sms < kMaxCtas ? 2 * sms : kMaxCtas);
+}
+
 }  // namespace sk

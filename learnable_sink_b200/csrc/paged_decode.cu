@@ -78,34 +78,13 @@ __device__ __forceinline__ bool visible(const PagedDecodeProblem& p, int n, int 
   return pos < n && (p.window <= 0 || pos < p.n_sink || pos >= n - p.window);
 }
 
-// A CTA's run of units, walked segment by segment (every role walks for itself).
+// Every role walks the CTA's run for itself.
 template <int TP>
-struct Walk {
-  int b, kvh, t0, cnt;  // the segment: tiles [t0, t0 + cnt) of (b, kvh)
-  SeqTiles seq;
-  int left;             // units of the run from the segment on
-  __device__ __forceinline__ void cut() {
-    cnt = min(seq.count - t0, left);
-  }
-  // a run that begins behind a pair's tiles begins with the next pair
-  __device__ __forceinline__ bool begin(const PagedDecodeProblem& p) {
-    return left > 0 && (cnt > 0 || next(p));
-  }
-  __device__ __forceinline__ bool next(const PagedDecodeProblem& p) {
-    left -= seq.count + kPairUnits - t0;
-    if (left <= 0) return false;
-    t0 = 0;
-    if ((kvh += p.lanes) >= p.c.Hkv) {
-      kvh -= p.c.Hkv;
-      seq = seq_tiles<TP>(p, ++b);
-    }
-    cut();
-    return true;
-  }
-};
-template <int TP>
+__device__ __forceinline__ bool next_segment(const PagedDecodeProblem& p, Walk& w) {
+  return w.next(p.c.Hkv, p.lanes, [&](int b) { return seq_tiles<TP>(p, b); });
+}
 struct Start {
-  Walk<TP> walk;
+  Walk walk;
   int first, total;  // the run's first unit; units of all
   bool whole;        // a pair a CTA
 };
@@ -113,7 +92,7 @@ struct Start {
 // Adds up the lengths (a slice of the sequences a thread) and finds where this
 // CTA's run begins; the thread whose slice it is in sets the walk up for all.
 template <int THREADS, int TP, int SLACK>
-__device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start<TP>* st, int2* s_warp) {
+__device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start* st, int2* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per_thread = (p.c.B + THREADS - 1) / THREADS;
   const int b0 = tid * per_thread, b1 = min(b0 + per_thread, p.c.B);
@@ -144,40 +123,17 @@ __device__ __forceinline__ void find_start(const PagedDecodeProblem& p, Start<TP
   total *= chunks;
   before *= chunks;
   const Runs runs(total, groups);
+  auto seq_of = [&](int b) { return seq_tiles<TP>(p, b); };
   if (rows_whole(p.c.B * chunks, longest, runs.per, groups, SLACK)) {
     if (tid == 0) {
-      Walk<TP> w;
-      w.b = group / chunks;
-      w.kvh = (group - w.b * chunks) * p.lanes + blockIdx.x;
-      w.t0 = w.left = 0;
-      if (w.b < p.c.B) {
-        w.seq = seq_tiles<TP>(p, w.b);
-        w.left = w.seq.count + kPairUnits;
-        w.cut();
-      }
-      st->walk = w;
+      st->walk = whole_walk(group, blockIdx.x, p.c.B, p.lanes, chunks, seq_of);
       st->whole = true;
     }
     return;
   }
   const int f0 = runs.begin(group);
   if (f0 >= before && f0 < before + sum * chunks) {
-    Walk<TP> w;
-    w.b = b0;
-    for (;;) {
-      w.seq = seq_tiles<TP>(p, w.b);
-      const int units = (w.seq.count + kPairUnits) * chunks;
-      if (f0 < before + units) break;
-      before += units;
-      ++w.b;
-    }
-    const int rem = f0 - before, units = w.seq.count + kPairUnits;
-    const int chunk = rem / units;
-    w.kvh = chunk * p.lanes + blockIdx.x;
-    w.t0 = rem - chunk * units;
-    w.left = runs.begin(group + 1) - f0;
-    w.cut();
-    st->walk = w;
+    st->walk = cut_walk(f0, runs.begin(group + 1) - f0, b0, before, blockIdx.x, p.lanes, chunks, seq_of);
     st->first = f0;
     st->total = total;
     st->whole = false;
@@ -379,7 +335,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   __shared__ Bars<SLOTS> bar;
   __shared__ int abort_s;
   __shared__ uint32_t tmem_s;
-  __shared__ Start<TP> start_s;
+  __shared__ Start start_s;
   __shared__ int2 warp_s[G_::WARPS];
   __shared__ __align__(16) float qs_s[8][GP];  // query scales of the last eight segments
   __shared__ float sink_sm[8][GP];             // their sink logits
@@ -434,9 +390,9 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   const uint32_t tmem = tmem_s;
   const uint32_t tm_s = tmem, tm_o = tmem + 2 * NT, tm_fold = tmem + 3 * NT;
 
-  Walk<TP> w = start_s.walk;
+  Walk w = start_s.walk;
   const int total = start_s.total, f0 = start_s.first, run = w.left;
-  const bool work = w.begin(p);
+  const bool work = w.begin(c.Hkv, p.lanes, [&](int b) { return seq_tiles<TP>(p, b); });
 
   if (!work) {
     // less work than CTAs
@@ -476,7 +432,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
                         nb * (G_::BW / G_::EB), 0, row);
         }
       }
-    } while (ok && w.next(p));
+    } while (ok && next_segment<TP>(p, w));
     // The join's CTAs come up under the last tiles (let up at the start, the work before
     // their wait is in this kernel's way: 0.2 to 0.4 us).
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -539,7 +495,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
           pend_first = i % kFold == 0;
         }
         ++seg;
-      } while (ok && w.next(p));
+      } while (ok && next_segment<TP>(p, w));
       if (ok && pend >= 0) issue_pv();
       if (!ok) {  // no product may be running when the tensor memory is freed
         mma_commit(&bar.drain);
@@ -635,7 +591,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.q_full[seg & 1]);
       ++seg;
-    } while (w.next(p));
+    } while (next_segment<TP>(p, w));
   } else if (warp == W_Q + 1) {
     // ---------------------------------------------------------------- page scales
     const int ppt = TP >> c.page_log2;
@@ -662,7 +618,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
           const int first = f0 + run - w.left, group = blockIdx.y;
           const Runs runs(total, gridDim.y);
           reinterpret_cast<int2*>(p.part)[pair] = make_int2(
-              group, start_s.whole ? 1 : runs.cta_of(first + w.seq.count - 1) - group + 1);
+              group, start_s.whole ? 1 : parts_of(runs, group, first, w.seq.count));
         }
         if (fresh(c.seqlens + w.b) > w.seq.n) set_status(c.status, SINKATTN_ERR_BOUNDS);
       }
@@ -683,7 +639,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.s_full[j & 1]);
       }
-    } while (ok && w.next(p));
+    } while (ok && next_segment<TP>(p, w));
   } else {
     // ---------------------------------------------------------------- softmax
     const int wg = NWG == 1 ? 0 : warp >> 2, wt = tid & 127, ww = warp & 3;
@@ -900,7 +856,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
       named_bar_sync(1 + wg, 128);
       const long long pair = (long long)w.b * c.Hkv + w.kvh;
       const bool final = w.cnt == w.seq.count;
-      float* part = parts + (pair + blockIdx.y * p.lanes) * G * (D + 2);
+      float* part = parts + part_slot(pair, blockIdx.y, p.lanes) * G * (D + 2);
       const long long row0 = (long long)w.b * p.Hq + w.kvh * G;
       if (wt < H && h0 + wt < G) {
         const int h = h0 + wt;
@@ -973,7 +929,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
         }
       }
       ++seg;
-    } while (w.next(p));
+    } while (next_segment<TP>(p, w));
   }
   __syncthreads();
   if (warp == W_MMA) {
@@ -1018,7 +974,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodePro
     if (!rows_whole(p.c.B * chunks, max(max(longest_s[0], longest_s[1]), max(longest_s[2], longest_s[3])),
                     runs.per, groups, SLACK)) {
       meta.x = runs.cta_of(first);
-      meta.y = runs.cta_of(first + mine_s - kPairUnits - 1) - meta.x + 1;
+      meta.y = parts_of(runs, meta.x, first, mine_s - kPairUnits);
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1027,7 +983,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodePro
   if (ns <= 1) return;
   const float* parts = p.part + meta_floats((long long)p.c.B * p.c.Hkv);
   const long long row = (long long)G * (D + 2), step = row * p.lanes;
-  const float* part = parts + pair * row + meta.x * step + (long long)(h % G) * (D + 2);
+  const float* part = parts + part_slot(pair, meta.x, p.lanes) * row + (long long)(h % G) * (D + 2);
   // the first segments' columns are on their way while the weights are made
   constexpr int U = 16;
   float v[U];
@@ -1104,8 +1060,7 @@ int decode_cfg(PagedDecodeProblem p, cudaStream_t stream) {
   if ((tiles + kPairUnits) * c.B * c.Hkv > INT_MAX) return SINKATTN_ERR_UNSUPPORTED;
   p.lanes = group_lanes(c.Hkv);
   p.chunks = c.Hkv / p.lanes;
-  const long long groups =
-      std::min<long long>((tiles + kPairUnits) * c.B * p.chunks, std::min(G_::CTAS * sms, kMaxCtas) / p.lanes);
+  const int groups = schedule_groups((tiles + kPairUnits) * c.B * p.chunks, G_::CTAS * sms, p.lanes);
   record_start(SINKATTN_KERNEL_DECODE, stream);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -1124,7 +1079,7 @@ int decode_cfg(PagedDecodeProblem p, cudaStream_t stream) {
   cfg.gridDim = dim3(c.B * p.Hq);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<E, D, G_::TP, G_::SLACK>, p, (int)groups) != cudaSuccess) return SINKATTN_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<E, D, G_::TP, G_::SLACK>, p, groups) != cudaSuccess) return SINKATTN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA;
 }
 
@@ -1144,7 +1099,7 @@ int decode_typed(const PagedDecodeProblem& p, cudaStream_t stream) {
 
 size_t paged_decode_part_floats(int B, int Hq, int Hkv, int D, int sms) {
   const long long pairs = (long long)B * Hkv;
-  return meta_floats(pairs) + (size_t)(min(2 * sms, kMaxCtas) + pairs) * (Hq / Hkv) * (D + 2);
+  return meta_floats(pairs) + (size_t)part_slots(pairs, sms) * (Hq / Hkv) * (D + 2);
 }
 
 int launch_paged_decode(const PagedDecodeProblem& p, cudaStream_t s) {

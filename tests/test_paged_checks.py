@@ -115,6 +115,18 @@ def test_decode_schedule_covers_every_position_once(tmp_path):
     assert out.returncode == 0 and out.stdout.startswith("ok "), out.stdout
 
 
+def test_decode_schedule_of_groups(tmp_path):
+    """The schedule as the kernels use it, by the functions that they call: groups of CTAs, rows
+    cut and rows left whole, partial slots, and the join's own reckoning of the segments."""
+    from learnable_sink_b200 import build
+    exe = str(tmp_path / "paged_groups_check")
+    subprocess.check_call([build.nvcc(), "-O2", "-std=c++17", "-arch=sm_100a", "--expt-relaxed-constexpr",
+                           "-I", os.path.join(ROOT, "include"),
+                           os.path.join(ROOT, "tests", "c", "paged_groups_check.cu"), "-o", exe])
+    out = subprocess.run([exe], capture_output=True, text=True)
+    assert out.returncode == 0 and out.stdout.startswith("ok "), out.stdout
+
+
 # ------------------------------------------------------------------ binding
 def _pool(dtype=bf, n=NP, h=Hkv, page=PAGE, d=D):
     return torch.zeros(n, h, page, d, dtype=dtype)
