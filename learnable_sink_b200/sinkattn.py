@@ -532,7 +532,8 @@ class PagedCache:
     ``v_scale`` [n_pages, Hkv]; ``block_table`` int32 [B, max_pages] and
     ``cache_seqlens`` int32 [B], which counts a call's new tokens.  The tensors
     are checked once, here, and kept: their contents may change between calls, the
-    attributes may not (other tensors are another PagedCache)."""
+    attributes and the tensors' storage (``set_``, ``resize_``) may not (other tensors
+    are another PagedCache)."""
 
     __slots__ = ("k_pages", "v_pages", "block_table", "cache_seqlens", "k_scale", "v_scale",
                  "device", "B", "Hkv", "D", "_c", "_ref", "_dev", "_at", "_kind")
@@ -582,6 +583,10 @@ class PagedCache:
         if hasattr(self, "_kind"):
             raise AttributeError(f"PagedCache.{name} is fixed; build another PagedCache")
         super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        # nor may a tensor be let go of: the descriptor holds its address
+        raise AttributeError(f"PagedCache.{name} is fixed; build another PagedCache")
 
 
 def _one_device(fn, *ts):

@@ -192,6 +192,15 @@ def test_cache_attributes_are_fixed(caches):
         assert c.cache_seqlens.tolist() == [0] * B
 
 
+def test_cache_attributes_stay(caches):
+    """Deleting an attribute would free memory that the descriptor names."""
+    for c in caches:
+        for name in ("k_pages", "block_table", "cache_seqlens", "_c", "_kind"):
+            with pytest.raises(AttributeError, match=name):
+                delattr(c, name)
+        assert c.k_pages.shape[0] == NP and c.cache_seqlens.tolist() == [0] * B
+
+
 def test_append_metadata_mismatches_are_refused(caches):
     c16, c8 = caches
     T = 7
