@@ -4,9 +4,10 @@
 
 Each .cu under csrc/ is compiled to an object (in parallel) and linked into
 learnable_sink_b200/libsinkattn.so.  Objects are rebuilt when their source
-or any header (csrc/*.cuh, csrc/*.h, include/*.h) is newer.  The Python side's
+or any header (csrc/*.cuh, csrc/*.h, include/*.h) is newer.  Then the Python side's
 own extension (csrc/binding.cpp: the short way for the paged calls) is compiled
-with g++ against torch's headers into learnable_sink_b200/_binding.so.
+with g++ against torch's headers into learnable_sink_b200/_binding.so, again for
+another torch, Python or compiler command.
 """
 from __future__ import annotations
 
@@ -24,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsinkattn.so")
 BINDING = os.path.join(PKG, "_binding.so")
+STAMP = os.path.join(OBJ, "binding.txt")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -65,32 +67,38 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
 
     import torch
     src = os.path.join(CSRC, "binding.cpp")
-    if not force and os.path.exists(BINDING) and \
-            os.path.getmtime(BINDING) >= max(os.path.getmtime(src), _newest_header()):
-        return BINDING
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
-    tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     for d in (os.path.join(home, "include"),
               os.path.join(home, "include", "torch", "csrc", "api", "include"),
               sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
         cmd += ["-isystem", d]
-    cmd += [src, "-o", tmp, "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu",
-            "-lc10", "-lc10_cuda"]
+    cmd += [src, "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda"]
+    # what the file was built with, beside the objects
+    stamp = "\n".join([torch.__version__, sys.version] + cmd) + "\n"
+    if not force and os.path.exists(BINDING) and \
+            os.path.getmtime(BINDING) >= max(os.path.getmtime(src), _newest_header()) and \
+            os.path.exists(STAMP) and open(STAMP).read() == stamp:
+        return BINDING
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd += ["-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if verbose or r.returncode != 0:
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
     if r.returncode != 0:
         raise RuntimeError("g++ failed on binding.cpp")
     os.replace(tmp, BINDING)
+    os.makedirs(OBJ, exist_ok=True)
+    with open(STAMP, "w") as f:
+        f.write(stamp)
     return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(OBJ, exist_ok=True)
-    build_binding(force, verbose)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(lambda s: _compile(s, force, verbose, extra), srcs))
@@ -102,6 +110,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, LIB)
+    build_binding(force, verbose)  # last: the library does not need it
     return LIB
 
 

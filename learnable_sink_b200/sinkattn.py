@@ -12,6 +12,7 @@ import contextlib
 import ctypes
 import math
 import os
+import warnings
 from dataclasses import dataclass
 from typing import Optional
 
@@ -121,16 +122,37 @@ def lib():
 _short = None
 
 
+class _PythonWay:
+    """Stands in for the extension where it cannot be used: every call is declined, and the
+    Python path makes it."""
+
+    @staticmethod
+    def paged_append(*args):
+        return -1
+
+    paged_decode = paged_append
+
+
 def _short_way():
     """The paged calls' short way (csrc/binding.cpp): it checks the tensors and
-    makes the C ABI call in one step, or declines (-1) without a launch."""
+    makes the C ABI call in one step, or declines (-1) without a launch.  Without the
+    extension, or with one that was built for another torch, the Python path makes every
+    call (the same kernels, some microseconds of host time more)."""
     global _short
     if _short is None:
+        why = None
         try:
             from . import _binding
-        except ImportError as e:
-            raise ImportError("learnable_sink_b200/_binding.so is missing or does not load: build it "
-                              "with `python -m learnable_sink_b200.build`") from e
+            if _binding.torch_version != torch.__version__.split("+")[0]:
+                why = f"was built for torch {_binding.torch_version}"
+        except (ImportError, AttributeError) as e:
+            why = f"is missing or does not load ({e})"
+        if why is not None:
+            warnings.warn(f"learnable_sink_b200/_binding.so {why}: build it with `python -m "
+                          "learnable_sink_b200.build`; the paged calls take longer on the host "
+                          "without it", RuntimeWarning, stacklevel=4)
+            _short = _PythonWay
+            return _short
         L = lib()
         _binding.bind(*(_c.cast(f, _vp).value for f in (
             L.sinkattn_paged_append, L.sinkattn_paged_append_fp8,

@@ -4,6 +4,8 @@ of the float64 oracle that the GPU tests compare with."""
 import ctypes
 import os
 import subprocess
+import sys
+import warnings
 
 import numpy as np
 import pytest
@@ -271,6 +273,63 @@ def test_short_way_declines_what_it_does_not_handle(caches):
     assert d(*head, q, None, 0, 0, None, q, q, q, q) == -1
     with pytest.raises(TypeError):
         d(1, 2)
+
+
+@pytest.mark.parametrize("broken", ["missing", "other torch"])
+def test_without_the_extension_the_python_path_makes_the_calls(caches, monkeypatch, broken):
+    """A missing _binding.so, or one of another torch, is said once and does not stop the calls."""
+    import learnable_sink_b200 as pkg
+    if broken == "missing":
+        monkeypatch.delattr(pkg, "_binding", raising=False)
+        monkeypatch.setitem(sys.modules, "learnable_sink_b200._binding", None)
+    else:
+        monkeypatch.setattr(torch, "__version__", "1.0.0+cpu")
+    monkeypatch.setattr(S, "_short", None)
+    c16, c8 = caches
+    k = torch.zeros(B, Hkv, D, dtype=bf)
+    q, z = torch.zeros(B, Hq, D, dtype=bf), torch.zeros(B, Hq)
+    with pytest.warns(RuntimeWarning, match="_binding.so"):
+        _refused(lambda: S.paged_append(k.half(), k.half(), c16), "k is")
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        _refused(lambda: S.paged_decode_fp8(q, c16, None, workspace=z, out=q, lse=z, sink_s=z),
+                 "not an 8-bit cache")
+
+
+def test_build_makes_the_library_before_the_extension(monkeypatch):
+    """Without g++ or torch's headers the library is built all the same, and the failure said."""
+    from learnable_sink_b200 import build
+    order = []
+    compile_ = build._compile
+
+    def no_extension(*a):
+        order.append("extension")
+        raise RuntimeError("g++ failed")
+
+    monkeypatch.setattr(build, "_compile", lambda *a: order.append("library") or compile_(*a))
+    monkeypatch.setattr(build, "build_binding", no_extension)
+    with pytest.raises(RuntimeError, match="g[+][+] failed"):
+        build.build()
+    assert order[0] == "library" and order[-1] == "extension" and order.count("extension") == 1
+    assert os.path.exists(build.LIB)
+
+
+def test_build_compiles_the_extension_again_for_another_torch(monkeypatch):
+    from learnable_sink_b200 import build
+    build.build_binding()
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        return subprocess.CompletedProcess(cmd, 1, "", "")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    build.build_binding()
+    assert not ran
+    monkeypatch.setattr(torch, "__version__", "1.0.0")
+    with pytest.raises(RuntimeError, match="binding"):
+        build.build_binding()
+    assert len(ran) == 1 and "binding.cpp" in " ".join(ran[0])
 
 
 # ------------------------------------------------------------------ the oracle
