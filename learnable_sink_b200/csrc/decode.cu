@@ -1130,9 +1130,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1) decode_fp8_kernel(
   }
 }
 
+}  // namespace
+
 // uint8 [T, H, D] map of E4M3 codes, one box of box_t rows x D bytes; the
 // 128-byte swizzle for 128-byte rows, the 64-byte swizzle for 64-byte rows.
-bool make_tmap_codes_impl(CUtensorMap* map, const void* base, int T, int H, int D, int box_t) {
+bool make_tmap_codes(CUtensorMap* map, const void* base, int T, int H, int D, int box_t) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
     cudaDriverEntryPointQueryResult q;
@@ -1151,6 +1153,8 @@ bool make_tmap_codes_impl(CUtensorMap* map, const void* base, int T, int H, int 
             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 template <int D, int G>
 int launch_fp8_cfg(const DecodeFp8Problem& q, cudaStream_t stream) {
@@ -1214,10 +1218,6 @@ int dispatch_g(const DecodeProblem& p, cudaStream_t stream) {
 }
 
 }  // namespace
-
-bool make_tmap_codes(CUtensorMap* map, const void* base, int T, int H, int D, int box_t) {
-  return make_tmap_codes_impl(map, base, T, H, D, box_t);
-}
 
 int launch_decode_fp8(const DecodeFp8Problem& q, cudaStream_t stream) {
   return q.base.D == 64 ? dispatch_fp8<64>(q, stream) : dispatch_fp8<128>(q, stream);
