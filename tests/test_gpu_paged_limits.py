@@ -305,3 +305,37 @@ def test_steps_whose_scales_grow(D, page):
     assert grown > 100
     assert np.array_equal(cache.k_pages.cpu().numpy(), kc) and np.array_equal(np64(cache.k_scale), ksn)
     assert np.array_equal(cache.v_pages.cpu().numpy(), vc) and np.array_equal(np64(cache.v_scale), vsn)
+
+
+@pytest.mark.parametrize("dtype,fp8", KINDS)
+@pytest.mark.parametrize("D,G", [(64, 8), (128, 4), (64, 16), (128, 16)])
+def test_decode_folded_sums_follow_the_references(dtype, fp8, D, G):
+    """Scores that rise twice, by 7 log2 units in all, behind the first folds of a row that is not
+    cut, and fall again: what was folded is brought along each time."""
+    n, page = 45000, 64
+    B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    p = Problem([n], G, 1, D, page, dtype, fp8, seed=91)
+    pages = p.table[0].long()
+    pos = torch.arange(pages.numel() * page).view(-1, page)
+    lift = (pos > 9000) * 2.0 + (pos > 20000) * 3.0 - (pos > 36000) * 6.0  # score units
+    p.q[:, :, 0] = 8.0
+    x = lift / (8.0 * p.scale)
+    if fp8:
+        keys = torch.randn(p.k.shape, generator=gen(92))
+        keys[pages, 0, :, 0] = x
+        p.ks[:] = 2.0 ** -5
+        p.k = (keys * 32).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        p.k[pages, 0, :, 0] = x.to(dtype)
+    want = p.want()
+    p.table, p.lens = p.table.expand(B, -1).contiguous(), p.lens.expand(B).contiguous()
+    p.q = p.q.expand(B, -1, -1).contiguous()
+    out, lse, ss = p.run()
+    assert all(torch.equal(t, t[:1].expand_as(t)) for t in (out, lse, ss))
+    top = np.abs((oracle.fp8_e4m3_value(p.v.numpy()) * p.vs.double().numpy()[:, :, None, None]) if fp8
+                 else np64(p.v)).max()
+    d = np.abs(np64(out[0]) - want[0][0])
+    tol = torch.finfo(dtype).eps / 2 * np.abs(want[0][0]) + 2.0 ** -12 * top
+    assert (d <= tol).all(), float((d / tol).max())
+    check_lse(np64(lse[0]), want[1][0], 2.0 ** -12)
+    assert np.abs(np64(ss[0]) - want[2][0]).max() <= 2.0 ** -12
