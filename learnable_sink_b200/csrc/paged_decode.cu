@@ -195,14 +195,18 @@ struct Geo {
 };
 
 // Probabilities are held as 2^kBase e^{x - m}: with a reference that lags by at
-// most 2^kLag they stay within 2^8 (E4M3 reaches 448), as high as they can.  The
+// most 2^kLag they stay within 2^8 (E4M3 reaches 448), as high as they can: f16 and E4M3
+// lose small ones.  bf16 does not, and its values reach as far as O, so there they stay
+// within 1.  The
 // 8-bit terms are split in f16 pairs, where a residue and its move by 2^5 are exact and
 // take half the instructions of float32.  What the rounding to f16 left is moved by 2^10
 // and goes into the third term, whose own residue is the fourth: at worst that is 512
 // and saturates, 64 2^-15 of a weight above 128, 2^-16 (a weight below its reference keeps
 // 2^-17.6).  The fourth term's last bit is 2^-24 in these units; half of it, and half of
 // that for f16's own subnormals, are below 2^-30 of the largest weight.
-constexpr float kLag = 2.f, kBase = 6.f;
+constexpr float kLag = 2.f;
+template <class E, bool F8>
+constexpr float kBase = F8 || E::kFmt == 0 ? 6.f : -kLag;
 
 // Tiles whose sums O and l are held as the tensor cores and the threads add them up: at
 // most 512 steps of O, each truncated by less than 2^-23 of it.
@@ -802,7 +806,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
             for (int k = 0; k < 2; ++k) {
               const float pr = fast_exp2(x[q][h + k] - ref[0][h + k]);
               l[h + k] += pr;
-              e[k] = F8 ? fast_exp2(x[q][h + k] + (lvs - ref[1][h + k] + kBase)) : pr * 64.f;
+              e[k] = F8 ? fast_exp2(x[q][h + k] + (lvs - ref[1][h + k] + kBase<E, F8>)) : pr * (E::kFmt == 0 ? 64.f : 0.25f);
             }
             if constexpr (F8) {
               __half2 v = __floats2half2_rn(e[0], e[1]);
@@ -870,11 +874,11 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
           const float mt = fmaxf(m, a2);
           const float lw = lt * ratio2(m, mt), den = lw + ratio2(a2, mt);
           const float inv = den != 0.f ? 1.f / den : 0.f;
-          f = mo == kNone ? inv : fast_exp2(mo - mt - kBase) * inv;
+          f = mo == kNone ? inv : fast_exp2(mo - mt - kBase<E, F8>) * inv;
           p.lse[row0 + h] = lse_of(lw, den, mt, a);
           if (p.sink_s) p.sink_s[row0 + h] = lw * inv;
         } else {
-          f = mo == kNone ? 1.f : fast_exp2(mo - m - kBase);
+          f = mo == kNone ? 1.f : fast_exp2(mo - m - kBase<E, F8>);
           part[h * (D + 2) + D] = m;
           part[h * (D + 2) + D + 1] = lt;
         }

@@ -339,3 +339,31 @@ def test_decode_folded_sums_follow_the_references(dtype, fp8, D, G):
     assert (d <= tol).all(), float((d / tol).max())
     check_lse(np64(lse[0]), want[1][0], 2.0 ** -12)
     assert np.abs(np64(ss[0]) - want[2][0]).max() <= 2.0 ** -12
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_values_at_the_end_of_the_range(fp8):
+    """Values of 1e38 and 3e38: a weight does not push their sums out of float32's range while
+    the sum of e^(x - m) v is inside."""
+    page = 16
+    g = gen(93)
+    lens = torch.tensor([1, 2, 1, 40], dtype=torch.int32)
+    table = torch.arange(4 * 3, dtype=torch.int32).view(4, 3)
+    k = torch.randn(12, 2, page, 128, generator=g)
+    v = torch.randn(12, 2, page, 128, generator=g).sign() * torch.tensor([3e38, 1e38, 1.5e38, 4e36]
+                                                                         ).repeat_interleave(3)[:, None, None, None]
+    q = torch.randn(4, 8, 128, generator=g).to(BF)
+    sc = ()
+    if fp8:
+        sc = (torch.full((12, 2), 2.0 ** -6), torch.full((12, 2), 2.0 ** 120))
+        k, v = (k * 64).to(torch.float8_e4m3fn), (v / 2.0 ** 120).to(torch.float8_e4m3fn)
+    else:
+        k, v = k.to(BF), v.to(BF)
+    cache = S.PagedCache(k.cuda(), v.cuda(), table.cuda(), lens.cuda(), *(t.cuda() for t in sc))
+    out, lse, _ = (S.paged_decode_fp8 if fp8 else S.paged_decode)(q.cuda(), cache, None)
+    codes = (t.view(torch.uint8) if fp8 else t for t in (k, v))
+    want = oracle.paged_decode(q, *codes, table, lens, 0, 0, None, 128 ** -0.5, *sc)
+    top = np.abs(want[0]).max(axis=(1, 2), keepdims=True)
+    d = np.abs(np64(out) - want[0])
+    assert (d <= 2.0 ** -8 * np.abs(want[0]) + 2.0 ** -10 * top).all(), (np64(out)[:, 0, 0], want[0][:, 0, 0])
+    check_lse(np64(lse), want[1], 2.0 ** -12)
