@@ -300,6 +300,8 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
+// The mark of a page that is not in the pool, a NaN that log2f does not return.
+constexpr uint32_t kOutside = 0xffffffffu;
 // The reference of a row that has seen nothing: low enough that every score
 // raises it, and finite, so that -inf minus it is -inf and not NaN.
 constexpr float kNone = -3e38f;
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
   // the result.
   __shared__ __align__(16) float ref_s[NWG][2][H], corr_s[NWG][2][H], red_s[NWG][4][2 * H], fac_s[NWG][H];
   __shared__ float fold_s[NWG][4][H];  // each warp's folded l
-  // a tile's pages: score factor and log2 of the value scale (NaN: outside the pool)
+  // a tile's pages: score factor and log2 of the value scale (kOutside: not in the pool)
   __shared__ float2 page_s[2][TP / 16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.Hq / p.c.Hkv;
@@ -635,7 +637,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
         }
         const bool outside = id == -1;
         id = load_id(i + 1);
-        v.y = outside ? __uint_as_float(0x7fffffffu) : F8 ? log2f(v.y) : 0.f;
+        v.y = outside ? __uint_as_float(kOutside) : F8 ? log2f(v.y) : 0.f;
         if (j >= 2) ok = mbar_wait(&bar.p_full[j & 1], ((j >> 1) - 1) & 1, &abort_s, c.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
           for (int h = 0; h < H; ++h) l[h] = 0.f;
         }
         const float2 page = page_s[j & 1][wt * PP >> c.page_log2];
-        const bool held = !isnan(page.y);
+        const bool held = __float_as_uint(page.y) != kOutside;
         const float lvs = held ? page.y : 0.f;
         // scores in log2 units; hidden positions at -inf whatever their rows hold
         bool seen[PP];

@@ -367,3 +367,18 @@ def test_decode_values_at_the_end_of_the_range(fp8):
     d = np.abs(np64(out) - want[0])
     assert (d <= 2.0 ** -8 * np.abs(want[0]) + 2.0 ** -10 * top).all(), (np64(out)[:, 0, 0], want[0][:, 0, 0])
     check_lse(np64(lse), want[1], 2.0 ** -12)
+
+
+@pytest.mark.parametrize("bits", [0x7FC00000, 0x7FFFFFFF, -1])
+def test_decode_value_scale_that_is_not_a_number(bits):
+    """A value scale of NaN or below 0 is outside the contract; it makes the page's head NaN and does
+    not hide its rows."""
+    p = Problem([100, 100], 8, 2, 64, 16, BF, True, seed=94)
+    want = p.want()
+    p.vs.view(torch.int32)[p.table[0, 3].long(), 1] = bits
+    p.vs[p.table[1, 2].long(), 0] = -1.0
+    out, lse, ss = p.run()
+    assert torch.isnan(out[0, 4:]).all() and torch.isnan(out[1, :4]).all()
+    assert torch.isfinite(out[0, :4]).all() and torch.isfinite(out[1, 4:]).all()
+    check_lse(np64(lse), want[1], 2.0 ** -12)
+    assert np.abs(np64(ss) - want[2]).max() <= 2.0 ** -12
