@@ -32,7 +32,7 @@
 // its own: a tile's time is latency, and four heads fit 80 registers, so the SM
 // holds enough warps to hide it (eight heads a thread: 1.6 times the time a tile).
 // Long sums are taken in two steps: the tensor cores truncate as they add, and a thread's
-// l takes a tile after the other, so every 64 tiles O and l are folded into sums that
+// l takes a tile after the other, so every 16 tiles O and l are folded into sums that
 // are rounded (262,144 equal weights in one row: the result is 1.0e-3 too small without).
 // In the 8-bit cache the value scale goes into the probability: e^{x - m} is
 // multiplied by it in the exponent, with a reference of its own.
@@ -209,8 +209,9 @@ template <class E, bool F8>
 constexpr float kBase = F8 || E::kFmt == 0 ? 6.f : -kLag;
 
 // Tiles whose sums O and l are held as the tensor cores and the threads add them up: at
-// most 512 steps of O, each truncated by less than 2^-23 of it.
-constexpr int kFold = 64;
+// most 128 steps of O, each truncated by less than 2^-23 of it.  (Folding costs a long 8-bit
+// decode 0.4 %, a 16-bit one nothing.)
+constexpr int kFold = 16;
 
 template <bool F8>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {

@@ -80,8 +80,8 @@ def test_append_rotates_infinities(dtype, D, inter):
 def test_decode_sums_over_a_long_row(fp8, D, G):
     """262,144 equal weights in a row that is not cut: the result is the values' mean, rounded
     once.  The tensor cores truncate a sum as they add to it (less than 2^-23 of it for
-    each step of 16 positions), over 64 tiles of 128 positions at most: 2^-14; the tiles'
-    sums and the weights' own add 2^-19."""
+    each step of 16 positions), over 16 tiles of 128 positions at most: 2^-16; the sums of
+    those, 128 at most, and the weights' own add 2^-17."""
     n, page = 262144, 128
     B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
     pages = n // page
@@ -100,15 +100,15 @@ def test_decode_sums_over_a_long_row(fp8, D, G):
     out, lse, _ = call(torch.ones(B, G, D, dtype=F16, device="cuda"), cache, None)
     want = value.mean((0, 1, 2))
     d = (out.double() / want - 1).abs().max().item()
-    assert d <= 2.0 ** -11 + 2.0 ** -14 + 2.0 ** -18, d
+    assert d <= 2.0 ** -11 + 2.0 ** -16 + 2.0 ** -17, d
     check_lse(np64(lse), np.full((B, G), np.log(n)), 2.0 ** -18)
 
 
 @pytest.mark.parametrize("D,n_sink,window", [(64, 0, 0), (128, 0, 0), (64, 4, 40000)])
 def test_decode_lse_of_small_weights_beside_a_dominant_one(D, n_sink, window):
     """The first token's weight is 1, every other one's 2^-20.3, in rows that are not cut: a
-    thread's sum begins with the large one, and the small ones must not be lost to it (64 of
-    them in a row lose at most 2^-18).  The scores are off by 2^-17.7 at most."""
+    thread's sum begins with the large one, and the small ones must not be lost to it (16 of
+    them in a row lose at most 2^-20).  The scores are off by 2^-17.7 at most."""
     n, page = 131072, 128
     B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
     k = torch.zeros(n // page, 1, page, D, dtype=BF, device="cuda")
@@ -132,7 +132,7 @@ def test_decode_small_weights_beside_a_dominant_one(dtype, fp8, D, n_sink, windo
     that none is cut.  Values are 0 in the first token's page and 1 elsewhere, so the output is the
     small weights' sum.  A weight is off by at most 2^-16 of itself and 2^-30 of the largest
     (the latter times 2^lift, the first page's value scale over the others'); the result is
-    rounded once more; the sums of 64 tiles (2^-14), their own and the scores' errors add less
+    rounded once more; the sums of 16 tiles (2^-16), their own and the scores' errors add less
     than 2^-12 of it."""
     n, page = 131072, 128
     B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
