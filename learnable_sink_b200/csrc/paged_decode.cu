@@ -306,9 +306,13 @@ constexpr uint32_t kOutside = 0xffffffffu;
 // The reference of a row that has seen nothing: low enough that every score
 // raises it, and finite, so that -inf minus it is -inf and not NaN.
 constexpr float kNone = -3e38f;
-// 2^(a - b), 0 from a = -inf (also over b = -inf), 1 from a = b = inf (a sink logit's)
+// 2^(a - b), 0 from a = -inf (also over b = -inf)
 __device__ __forceinline__ float ratio2(float a, float b) {
-  return a == -INFINITY ? 0.f : a == b ? 1.f : fast_exp2(a - b);
+  return a == -INFINITY ? 0.f : fast_exp2(a - b);
+}
+// the sink's over the maximum, which it may be itself, at +inf too
+__device__ __forceinline__ float sink_ratio(float a2, float mt) {
+  return a2 == INFINITY ? 1.f : ratio2(a2, mt);
 }
 // log(lw 2^mt + e^a), den = lw + e^a / 2^mt: a itself, whatever its size, where the keys have
 // no weight beside it
@@ -875,7 +879,7 @@ __global__ void __launch_bounds__(Geo<E, D, F8, NWG>::THREADS, Geo<E, D, F8, NWG
         if (final) {
           const float a = sink_sm[seg & 7][h], a2 = a * kLog2e;
           const float mt = fmaxf(m, a2);
-          const float lw = lt * ratio2(m, mt), den = lw + ratio2(a2, mt);
+          const float lw = lt * ratio2(m, mt), den = lw + sink_ratio(a2, mt);
           const float inv = den != 0.f ? 1.f / den : 0.f;
           f = mo == kNone ? inv : fast_exp2(mo - mt - kBase<E, F8>) * inv;
           p.lse[row0 + h] = lse_of(lw, den, mt, a);
@@ -1026,7 +1030,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedDecodePro
   if (lane == 0) red_s[1][warp] = lt;
   __syncthreads();
   lt = (red_s[1][0] + red_s[1][1]) + (red_s[1][2] + red_s[1][3]);
-  const float den = lt + ratio2(a2, mt);
+  const float den = lt + sink_ratio(a2, mt);
   const long long at = (long long)b * p.Hq + h;
   if (tid < D) {
     float o = 0.f;
