@@ -269,7 +269,7 @@ __device__ __forceinline__ void token_rows(const PagedAppendProblem& p, int t, i
 
 constexpr int kAppendThreads = 256;
 // Bound by HBM: 411 MB (4 x 4,096 tokens, 32 query and 2 x 8 key and value heads of
-// 128) in 66 us, 6.2 TB/s, 0.95 of a plain copy's rate.  Rows in flight a thread and
+// 128) in 66 to 67 us, 6.2 TB/s, 0.94 of a plain copy's rate.  Rows in flight a thread and
 // blocks an SM: more rows hide latency within a thread, but their registers cost the
 // threads that hide it beside them.  (2, 4) takes 66 us there, (4, 3) 69, (4, 2) 78,
 // (1, 6) 71; a ragged batch at D = 64 takes 36 us with (4, 3) and 40 with (4, 2), (4, 4).
@@ -330,10 +330,10 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float m) {
 // registers between the block's amax and the encoding: two passes of a warp over a
 // head of 128, or one over two heads of 64, which then share their angles and the
 // block's beginning.  That is what 64 registers hold.  A prefill of 4 x 4,096 tokens, 8
-// heads of 128, takes 68 us so, 88 with sixteen rows a warp (128 registers), 76 with
+// heads of 128, takes 68 to 70 us so, 88 with sixteen rows a warp (128 registers), 76 with
 // four rows of two heads; a ragged batch at D = 64 26 us, 28 with one head.  It is bound
 // by its instructions and by the chain of small loads (offsets, length, table) that a
-// block begins with: the prefill without queries takes 30 us for 100 MB, 26 without the
+// block begins with: the prefill without queries takes 30 us for 100 MB, 25 without the
 // rotation, whose angles every head's block reads again.  Other blocks rotate the
 // queries.
 //

@@ -7,8 +7,8 @@
 // Bound by HBM (a visible row of K and V is read once and shared by the G query
 // heads of its KV head), as long as the arithmetic stays off the CUDA cores: 16
 // sequences of 8 to 32 thousand tokens, 8 KV heads of 128, take 195 to 202 us (6.6 to
-// 6.9 TB/s; a plain copy reaches 6.5), 4 of 98 to 131 thousand in 8 bits 139 to 143 us
-// (6.6 to 6.8 TB/s).  A call of little work takes 7.1 us: 1 to find its place from the
+// 6.9 TB/s; a plain copy reaches 6.5), 4 of 98 to 131 thousand in 8 bits 139 to 144 us
+// (6.5 to 6.8 TB/s).  A call of little work takes 7.2 us: 1 to find its place from the
 // lengths, 1.6 until the first scores, 1.5 for a tile and its result, 1 to end the
 // kernel, 1.7 to join.  So
 // both products run on tcgen05 with the cache as the M side, where its rows lie
@@ -33,7 +33,8 @@
 // holds enough warps to hide it (eight heads a thread: 1.6 times the time a tile).
 // Long sums are taken in two steps: the tensor cores truncate as they add, and a thread's
 // l takes a tile after the other, so every 16 tiles O and l are folded into sums that
-// are rounded (262,144 equal weights in one row: the result is 1.0e-3 too small without).
+// are rounded (262,144 equal weights in one row: the result is up to 1.4e-3 too small
+// without).
 // In the 8-bit cache the value scale goes into the probability: e^{x - m} is
 // multiplied by it in the exponent, with a reference of its own.
 //
