@@ -119,13 +119,14 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // fused multiply-add gives them), which leaves half a unit in the last place or
 // little more whatever cancels: an 8-bit code next to a tie then falls as the exact
 // value does.  16-bit results do not show the difference.  The error of an infinite
-// product is NaN; the maximum with a finite number (below any other error) drops it, and
+// product is not a number, or infinite where the product overflowed; it is left out, and
 // the sum stays infinite, or NaN where two infinities cancel.
 template <bool EXACT>
 __device__ __forceinline__ float turn(float x, float c, float y, float s) {
   if constexpr (!EXACT) return x * c + y * s;
   const float w = y * s, e = fmaf(y, s, -w);
-  return fmaf(x, c, w) + fmaxf(e, -3.4e38f);
+  const float r = fmaf(x, c, w);
+  return fabsf(w) < INFINITY ? r + e : r;
 }
 template <bool EXACT>
 __device__ __forceinline__ void rotate_pairs(float (&x)[8], const float* c, const float* s) {

@@ -382,3 +382,30 @@ def test_decode_value_scale_that_is_not_a_number(bits):
     assert torch.isfinite(out[0, :4]).all() and torch.isfinite(out[1, 4:]).all()
     check_lse(np64(lse), want[1], 2.0 ** -12)
     assert np.abs(np64(ss) - want[2]).max() <= 2.0 ** -12
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_append_rotation_that_overflows(inter, sign):
+    """A rotation table with a factor of its own, and keys near the end of bf16's range: a product
+    beyond float32 is infinite with its sign, and saturates; it is not NaN."""
+    rot, D = 16, 64
+    rope = torch.tensor([[0.5] * 8 + [1.5 * sign] * 8])
+    x = torch.zeros(1, 2, D, dtype=BF)
+    x[:, 0, :rot] = 3.3e38
+    x[:, :, 40] = 100.0
+    one = torch.ones(1, dtype=torch.int32).cuda()
+    codes = torch.zeros(1, 1, 16, D, dtype=torch.uint8).cuda()
+    cache = S.PagedCache(codes, codes.clone(), torch.zeros(1, 1, dtype=torch.int32).cuda(), one,
+                         torch.zeros(1, 1).cuda(), torch.zeros(1, 1).cuda())
+    k_out = torch.empty(1, 1, D, dtype=BF, device="cuda")
+    xd = x.cuda()
+    S.paged_append_fp8(xd[:, :1], xd[:, 1:], cache, None, rope.cuda(), inter, k_out=k_out)
+    torch.cuda.synchronize()
+    # a' = 0.5 a - 1.5 sign b, b' = 0.5 b + 1.5 sign a: the second product is +-infinite
+    a = torch.arange(0, rot, 2) if inter else torch.arange(rot // 2)
+    b = a + 1 if inter else a + rot // 2
+    up, down = (0x7E, 0xFE) if sign > 0 else (0xFE, 0x7E)
+    assert float(cache.k_scale) == 0.25
+    assert (codes[0, 0, 0, a.cuda()] == down).all() and (codes[0, 0, 0, b.cuda()] == up).all()
+    assert (k_out[0, 0, a.cuda()] == -sign * float("inf")).all() and (k_out[0, 0, b.cuda()] == sign * float("inf")).all()
