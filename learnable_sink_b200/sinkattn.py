@@ -143,7 +143,7 @@ def _short_way():
         why = None
         try:
             from . import _binding
-            if _binding.torch_version != torch.__version__.split("+")[0]:
+            if not torch.__version__.startswith(_binding.torch_version):  # 2.11.0+cu128, 2.12.0a0
                 why = f"was built for torch {_binding.torch_version}"
         except (ImportError, AttributeError) as e:
             why = f"is missing or does not load ({e})"
