@@ -512,10 +512,10 @@ int sinkattn_paged_append_fp8(sinkattn_dtype dt, int T, int Hq, const sinkattn_p
  *   learnable_sink, out, lse_new, sink_s  as for sinkattn_decode.  A sequence
  *                  that sees no key gets out = 0, lse = a_h (-inf without a
  *                  sink), sink_s = 0; so does one whose keys have no weight
- *                  beside e^(a_h), a_h = +inf among them.  What masked rows hold, NaN included, does
- *                  not matter.  An infinite visible value makes its element of
- *                  out infinite or NaN (a weight is two 16-bit terms, the second
- *                  of any sign or 0).
+ *                  beside e^(a_h), a_h = +inf among them.  What masked rows
+ *                  hold, NaN included, does not matter.  An infinite visible
+ *                  value makes its element of out infinite or NaN (a weight is
+ *                  two 16-bit terms, the second of any sign or 0).
  *   workspace      at least sinkattn_paged_decode_workspace_bytes bytes, any
  *                  contents; not shared by calls that may overlap.
  * The work is divided over the GPU from the sequences' lengths on the device, so

@@ -198,9 +198,9 @@ struct Geo {
 // Probabilities are held as 2^kBase e^{x - m}: with a reference that lags by at
 // most 2^kLag they stay within 2^8 (E4M3 reaches 448), as high as they can: f16 and E4M3
 // lose small ones.  bf16 does not, and its values reach as far as O, so there they stay
-// within 1.  The
-// 8-bit terms are split in f16 pairs, where a residue and its move by 2^5 are exact and
-// take half the instructions of float32.  What the rounding to f16 left is moved by 2^10
+// within 1.
+// The 8-bit terms are split in f16 pairs, where a residue and its move by 2^5 are exact
+// and take half the instructions of float32.  What the rounding to f16 left is moved by 2^10
 // and goes into the third term, whose own residue is the fourth: at worst that is 512
 // and saturates, 64 2^-15 of a weight above 128, 2^-16 (a weight below its reference keeps
 // 2^-17.6).  The fourth term's last bit is 2^-24 in these units; half of it, and half of
